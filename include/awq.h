@@ -416,6 +416,54 @@ awq_status w4a16_gemm_ws(const uint16_t* A, int64_t M, int64_t N, int64_t K, int
 awq_status awq_act_stats_noalloc(const void* X, awq_dtype xdt, int64_t M, int64_t K,
                                  int64_t ldx, float* sx, uint32_t* flags, hipStream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * awq_fp8_quantize -- a matrix in 8 bits: e4m3 codes (largest value 448, NaN 0x7F, no infinity)
+ * with one fp32 scale per block of 128 columns by 1 row (activations) or by 128 rows (weights).
+ * X        [M, K] with row stride ldx elements (ldx >= K, ldx % 8 == 0), dtype xdt (AWQ_F16,
+ *          AWQ_BF16 or AWQ_F32), 16-byte aligned; M >= 1, K >= 16, K % 16 == 0 (the last block of
+ *          a row, and of 128 rows, may be partial).
+ * block_rows  1 or 128.
+ * q        out, uint8 [M, K], 16-byte aligned: the e4m3 value nearest to x / scale, ties to even.
+ * scales   out, fp32 [ceil(M / block_rows), ceil(K / 128)]: 2^e with the smallest e >= -126 for
+ *          which the block's largest finite |x| is at most 448 2^e; 1 for a block without a
+ *          non-zero finite value. A power of two: x / scale is exact, and code * scale is exact
+ *          in bf16 and fp32.
+ * flags    in/out: NONFINITE_X (an Inf or NaN, whose code is NaN; the block's scale is that of its
+ *          finite values).
+ * Errors: AWQ_ERR_NULL, AWQ_ERR_DTYPE, AWQ_ERR_CONFIG (block_rows), AWQ_ERR_SHAPE (sizes, ldx,
+ *         misalignment; more than 2^31 blocks of one row).
+ * ---------------------------------------------------------------------------------------- */
+awq_status awq_fp8_quantize(const void* X, awq_dtype xdt, int64_t M, int64_t K, int64_t ldx,
+                            int32_t block_rows, uint8_t* q, float* scales, uint32_t* flags,
+                            hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * awq_fp8_dequantize -- out[m, k] = code * scales[m / block_rows, k / 128], dense [M, K] in odt
+ * (AWQ_F16, AWQ_BF16 or AWQ_F32), rounded once. Any fp32 scales. Sizes, alignment and errors as
+ * awq_fp8_quantize.
+ * ---------------------------------------------------------------------------------------- */
+awq_status awq_fp8_dequantize(const uint8_t* q, const float* scales, int64_t M, int64_t K,
+                              int32_t block_rows, awq_dtype odt, void* out, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * awq_fp8_gemm -- the product of two 8-bit matrices,
+ *   Y[m,n] = sum_k a8[m,k] a_scales[m, k/128] w8[n,k] w_scales[n/128, k/128].
+ * A8       uint8 [M, K] e4m3 codes, a_scales fp32 [M, ceil(K/128)] (awq_fp8_quantize, block_rows
+ *          1); W8 uint8 [N, K], w_scales fp32 [ceil(N/128), ceil(K/128)] (block_rows 128). The
+ *          scales may be any fp32 numbers. Codes 16-byte aligned.
+ * Y        out, [M, N] in ydt (AWQ_F16 or AWQ_BF16), 16-byte aligned; fp32 sums, rounded once.
+ * ws       device workspace, 16-byte aligned, of at least awq_fp8_gemm_workspace_bytes(M, N, K)
+ *          bytes (0: ws may be NULL): scratch for the partial sums of K slices (M > 64 while the
+ *          output tiles number fewer than the CUs), which are added in a fixed order. Calls that
+ *          share a workspace must not overlap.
+ * Errors: AWQ_ERR_NULL, AWQ_ERR_DTYPE, AWQ_ERR_SHAPE (M < 1, N < 1, K < 16, K % 16, K > 2^20,
+ *         M N > 2^38, misalignment), AWQ_ERR_WORKSPACE.
+ * ---------------------------------------------------------------------------------------- */
+size_t awq_fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
+awq_status awq_fp8_gemm(const uint8_t* A8, const float* a_scales, const uint8_t* W8,
+                        const float* w_scales, int64_t M, int64_t N, int64_t K, awq_dtype ydt,
+                        void* Y, void* ws, size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -78,6 +78,10 @@ SIGNATURES = {
     "w4a16_gemm_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32]),
     "w4a16_gemm_ws": (_E, [_P, _I64, _I64, _I64, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "awq_act_stats_noalloc": (_E, [_P, _E, _I64, _I64, _I64, _P, _P, _P]),
+    "awq_fp8_quantize": (_E, [_P, _E, _I64, _I64, _I64, _I32, _P, _P, _P, _P]),
+    "awq_fp8_dequantize": (_E, [_P, _P, _I64, _I64, _I32, _E, _P, _P]),
+    "awq_fp8_gemm_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "awq_fp8_gemm": (_E, [_P, _P, _P, _P, _I64, _I64, _I64, _E, _P, _P, _SZ, _P]),
 }
 
 # bytes of the library's static scratch array (AWQ_NOALLOC_SCRATCH_BYTES in awq.h)

@@ -442,3 +442,129 @@ def w4a16_gemm_ws(A: torch.Tensor, qweight: torch.Tensor, scales16: torch.Tensor
         s16.data_ptr() if s16 is not None else None, out.data_ptr(), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream(A)))
     return out
+
+
+FP8 = torch.float8_e4m3fn
+
+
+@dataclasses.dataclass
+class Fp8Result:
+    q: torch.Tensor        # float8_e4m3fn [M, K]
+    scales: torch.Tensor   # fp32 [ceil(M / block_rows), ceil(K / 128)], powers of two
+    flags: torch.Tensor
+
+
+def _same_device(ref: torch.Tensor, *named) -> None:
+    for t, nm in named:
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{nm} must be on {ref.device}")
+
+
+def _out(out, shape, dtype, device) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _dev(out, "out")
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device:
+        raise ValueError(f"out must be {dtype} {tuple(shape)} on {device}")
+    return out
+
+
+def _scratch(workspace, nbytes: int, device):
+    """A workspace of `nbytes`: the caller's (checked), or one of this call's own from torch's
+    allocator, which orders its reuse by stream and keeps a captured graph's apart."""
+    if workspace is not None:
+        _dev(workspace, "workspace")
+        if workspace.device != device or workspace.numel() * workspace.element_size() < nbytes:
+            raise ValueError(f"workspace must hold {nbytes} bytes on {device}")
+        return workspace
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _blocks_shape(M: int, K: int, block_rows: int):
+    return ((M + block_rows - 1) // block_rows, (K + 127) // 128)
+
+
+def _fp8_check(q, scales, block_rows, name):
+    _dev(q, name)
+    _dev(scales, f"{name} scales")
+    if q.dim() != 2 or q.dtype != FP8:
+        raise ValueError(f"{name} must be float8_e4m3fn [rows, columns]")
+    if scales.dtype != torch.float32 or \
+            tuple(scales.shape) != _blocks_shape(q.shape[0], q.shape[1], block_rows):
+        raise ValueError(f"{name}: the scales must be fp32, one per block of {block_rows} x 128")
+
+
+def fp8_quantize(X: torch.Tensor, block_rows: int = 1,
+                 flags: torch.Tensor | None = None) -> Fp8Result:
+    """X in 8 bits: e4m3 codes with one power-of-two scale per block of 128 columns by 1 row
+    (activations) or 128 rows (weights). X may be a row-strided view (unit column stride, row
+    stride a multiple of 8 elements); its columns are a multiple of 16."""
+    lib = _lib.load()
+    if not X.is_cuda or X.dim() != 2 or (X.stride(1) != 1 and X.shape[1] > 1):
+        raise ValueError("X must be a 2-D device tensor with unit column stride")
+    if X.dtype not in _DT:
+        raise ValueError("X must be fp16, bf16 or fp32")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    M, K = X.shape
+    dev = X.device
+    flags = _flags(dev, flags)
+    _same_device(X, (flags, "flags"))
+    q = torch.empty((M, K), dtype=FP8, device=dev)
+    scales = torch.empty(_blocks_shape(M, K, block_rows), dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        check("awq_fp8_quantize", lib.awq_fp8_quantize(
+            X.data_ptr(), _DT[X.dtype], M, K, X.stride(0) if M > 1 else K, block_rows,
+            q.data_ptr(), scales.data_ptr(), flags.data_ptr(), _stream(X)))
+    return Fp8Result(q, scales, flags)
+
+
+def fp8_dequantize(q: torch.Tensor, scales: torch.Tensor, block_rows: int = 1,
+                   dtype: torch.dtype = torch.float16,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values code * scale of fp8_quantize's result, in `dtype`."""
+    lib = _lib.load()
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    _fp8_check(q, scales, block_rows, "q")
+    if dtype not in _DT:
+        raise ValueError("dtype must be fp16, bf16 or fp32")
+    _same_device(q, (scales, "scales"))
+    M, K = q.shape
+    out = _out(out, (M, K), dtype, q.device)
+    with torch.cuda.device(q.device):
+        check("awq_fp8_dequantize", lib.awq_fp8_dequantize(
+            q.data_ptr(), scales.data_ptr(), M, K, block_rows, _DT[dtype], out.data_ptr(),
+            _stream(q)))
+    return out
+
+
+def fp8_gemm_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Bytes of the fp8_gemm workspace for these sizes (0: none needed)."""
+    return int(_lib.load().awq_fp8_gemm_workspace_bytes(M, N, K))
+
+
+def fp8_gemm(A8: torch.Tensor, a_scales: torch.Tensor, W8: torch.Tensor, w_scales: torch.Tensor,
+             out_dtype: torch.dtype = torch.float16, out: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Y = (A8 a_scales) (W8 w_scales)^T, fp16 or bf16 [M, N], from fp8_quantize's formats: A8 in
+    blocks of 1 x 128, W8 [N, K] in blocks of 128 x 128."""
+    lib = _lib.load()
+    _fp8_check(A8, a_scales, 1, "A8")
+    _fp8_check(W8, w_scales, 128, "W8")
+    M, K = A8.shape
+    N = W8.shape[0]
+    if W8.shape[1] != K:
+        raise ValueError("A8 and W8 must have the same number of columns")
+    if out_dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("out_dtype must be fp16 or bf16")
+    dev = A8.device
+    _same_device(A8, (a_scales, "a_scales"), (W8, "W8"), (w_scales, "w_scales"))
+    out = _out(out, (M, N), out_dtype, dev)
+    ws = _scratch(workspace, lib.awq_fp8_gemm_workspace_bytes(M, N, K), dev)
+    with torch.cuda.device(dev):
+        check("awq_fp8_gemm", lib.awq_fp8_gemm(
+            A8.data_ptr(), a_scales.data_ptr(), W8.data_ptr(), w_scales.data_ptr(), M, N, K,
+            _DT[out_dtype], out.data_ptr(), ws.data_ptr() if ws is not None else None,
+            ws.numel() * ws.element_size() if ws is not None else 0, _stream(A8)))
+    return out

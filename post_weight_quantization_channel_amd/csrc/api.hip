@@ -578,4 +578,68 @@ awq_status w4a16_gemm_ws(const uint16_t* A, int64_t M, int64_t N, int64_t K, int
                                              ws, ws_bytes, stream));
 }
 
+namespace {
+
+// 8-bit operands: rows of K codes, K a multiple of 16, so that rows and 16-byte chunks stay
+// aligned; 256 rows of a tile must fit a 32-bit buffer range.
+constexpr int64_t kMaxFp8K = int64_t(1) << 20;
+
+bool fp8_matrix_ok(int64_t M, int64_t K, int32_t block_rows) {
+  return M >= 1 && K >= 16 && K % 16 == 0 && M <= kMaxDim && K <= kMaxDim &&
+         M * ((K + 127) / 128) <= (int64_t(1) << 31) && (block_rows == 1 || block_rows == 128);
+}
+
+awq_status check_fp8_gemm(int64_t M, int64_t N, int64_t K) {
+  if (M < 1 || N < 1 || K < 16 || K % 16 || M > kMaxDim || N > kMaxDim || K > kMaxFp8K ||
+      M * N > (int64_t(1) << 38))
+    return AWQ_ERR_SHAPE;
+  return AWQ_OK;
+}
+
+}  // namespace
+
+awq_status awq_fp8_quantize(const void* X, awq_dtype xdt, int64_t M, int64_t K, int64_t ldx,
+                            int32_t block_rows, uint8_t* q, float* scales, uint32_t* flags,
+                            hipStream_t stream) {
+  if (!X || !q || !scales || !flags) return AWQ_ERR_NULL;
+  if (!valid_dtype(xdt)) return AWQ_ERR_DTYPE;
+  if (block_rows != 1 && block_rows != 128) return AWQ_ERR_CONFIG;
+  if (!fp8_matrix_ok(M, K, block_rows) || ldx < K || ldx % 8 || ldx > kMaxDim || !aligned16(X) ||
+      !aligned16(q) || (reinterpret_cast<uintptr_t>(scales) & 3u))
+    return AWQ_ERR_SHAPE;
+  return hip_status(awq::launch_fp8_quantize(X, (int)xdt, M, K, ldx, block_rows, q, scales, flags,
+                                             stream));
+}
+
+awq_status awq_fp8_dequantize(const uint8_t* q, const float* scales, int64_t M, int64_t K,
+                              int32_t block_rows, awq_dtype odt, void* out, hipStream_t stream) {
+  if (!q || !scales || !out) return AWQ_ERR_NULL;
+  if (!valid_dtype(odt)) return AWQ_ERR_DTYPE;
+  if (block_rows != 1 && block_rows != 128) return AWQ_ERR_CONFIG;
+  if (!fp8_matrix_ok(M, K, block_rows) || !aligned16(q) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(scales) & 3u))
+    return AWQ_ERR_SHAPE;
+  return hip_status(awq::launch_fp8_dequantize(q, scales, M, K, block_rows, (int)odt, out, stream));
+}
+
+size_t awq_fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return check_fp8_gemm(M, N, K) == AWQ_OK ? awq::fp8_gemm_plan(M, N, K).ws_bytes : 0;
+}
+
+awq_status awq_fp8_gemm(const uint8_t* A8, const float* a_scales, const uint8_t* W8,
+                        const float* w_scales, int64_t M, int64_t N, int64_t K, awq_dtype ydt,
+                        void* Y, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!A8 || !a_scales || !W8 || !w_scales || !Y) return AWQ_ERR_NULL;
+  if (ydt != AWQ_F16 && ydt != AWQ_BF16) return AWQ_ERR_DTYPE;
+  const awq_status cs = check_fp8_gemm(M, N, K);
+  if (cs != AWQ_OK) return cs;
+  if (!aligned16(A8) || !aligned16(W8) || !aligned16(Y) ||
+      (reinterpret_cast<uintptr_t>(a_scales) & 3u) || (reinterpret_cast<uintptr_t>(w_scales) & 3u))
+    return AWQ_ERR_SHAPE;
+  const size_t need = awq::fp8_gemm_plan(M, N, K).ws_bytes;
+  if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws))) return AWQ_ERR_WORKSPACE;
+  return hip_status(awq::launch_fp8_gemm(A8, a_scales, W8, w_scales, M, N, K, (int)ydt,
+                                         static_cast<uint16_t*>(Y), ws, stream));
+}
+
 }  // extern "C"

@@ -193,4 +193,24 @@ hipError_t launch_w4a16(const uint16_t* A, int64_t M, int64_t N, int64_t K, int 
                         const uint32_t* qweight, const uint16_t* scales16, const uint8_t* zeros,
                         const uint16_t* s16, uint16_t* Y, hipStream_t stream);
 
+// ---- 8-bit block format (fp8.hip): e4m3 codes, one fp32 scale per block_rows (1 or 128) x 128 ----
+hipError_t launch_fp8_quantize(const void* X, int dtype, int64_t M, int64_t K, int64_t ldx,
+                               int block_rows, uint8_t* q, float* scales, uint32_t* flags,
+                               hipStream_t stream);
+hipError_t launch_fp8_dequantize(const uint8_t* q, const float* scales, int64_t M, int64_t K,
+                                 int block_rows, int dtype, void* out, hipStream_t stream);
+
+// ---- product of two 8-bit operands (fp8_gemm.hip) ----
+struct Fp8GemmPlan {
+  int tile;          // square tile of the tiled kernel (M > 64)
+  int64_t S;         // K slices
+  int64_t steps;     // 128-channel steps per slice
+  int64_t stride;    // M N rounded up to a multiple of 4
+  size_t ws_bytes;   // 0 when S == 1
+};
+Fp8GemmPlan fp8_gemm_plan(int64_t M, int64_t N, int64_t K);
+hipError_t launch_fp8_gemm(const uint8_t* A, const float* sa, const uint8_t* W, const float* sw,
+                           int64_t M, int64_t N, int64_t K, int dtype, uint16_t* Y, void* ws,
+                           hipStream_t stream);
+
 }  // namespace awq
