@@ -83,9 +83,10 @@ enum {
   AWQ_FLAG_CLIP_RANGE = 1u << 8,       /* a clip ratio given to awq_pack_int4 is outside (0, 1]; */
                                        /* that group was packed unclipped                       */
   AWQ_FLAG_FOLD_RANGE = 1u << 9,       /* awq_fold_scale turned a finite parameter into Inf      */
-  AWQ_FLAG_NO_GRAM = 1u << 10          /* awq_clip_search_gram: the workspace holds no operand of */
+  AWQ_FLAG_NO_GRAM = 1u << 10,         /* awq_clip_search_gram: the workspace holds no operand of */
                                        /* a Gram-form search with this K and n_grid; nothing was */
                                        /* written                                                */
+  AWQ_FLAG_NONFINITE_ACT = 1u << 11    /* w4a16_gated_ckpt: g or u holds an Inf or NaN           */
 };
 
 /* How awq_search_layer evaluates the loss (same value, different contraction):
@@ -463,6 +464,89 @@ size_t awq_fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 awq_status awq_fp8_gemm(const uint8_t* A8, const float* a_scales, const uint8_t* W8,
                         const float* w_scales, int64_t M, int64_t N, int64_t K, awq_dtype ydt,
                         void* Y, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * w4a16_gated -- the gated feed-forward block on two packed weights that read one input,
+ *   g = A Wg^T, u = A Wu^T, H = act(g) u,  W[n,k] = c(q[n,k]) scales16[n, k/group]
+ * (codes as in w4a16_gemm), both projections, the activation and the product in one pass; g and u
+ * stay fp32 until H is rounded to fp16. Gate and up share their input and so one s, which is
+ * folded into the operator that produces it (awq_search_layers, awq_fold_scale): A comes divided.
+ * A        fp16 bits [M, K]; H out, fp16 bits [M, N]; both 16-byte aligned.
+ * gate, up host structs (read during the call) of device pointers, as w4a16_gemm's arguments:
+ *          both with zeros, or both without.
+ * act      AWQ_ACT_SILU: g / (1 + exp(-g)); AWQ_ACT_GELU: 0.5 g (1 + tanh(sqrt(2/pi) (g +
+ *          0.044715 g^3))).
+ * ws       device workspace, 16-byte aligned, of at least w4a16_gated_workspace_bytes(M, N, K, 0)
+ *          bytes (0: ws may be NULL): fp32 partials of g and u when K is split over workgroups
+ *          (M > 32 while the tiles leave CUs idle), added in a fixed order. Calls that share a
+ *          workspace must not overlap.
+ * Errors: AWQ_ERR_NULL, AWQ_ERR_CONFIG (group, act, zeros on one side only), AWQ_ERR_SHAPE (M < 1,
+ *         N < 1, K % 128, K > 32768, M N > 2^38, misalignment), AWQ_ERR_WORKSPACE.
+ * ---------------------------------------------------------------------------------------- */
+enum { AWQ_ACT_SILU = 0, AWQ_ACT_GELU = 1 };
+typedef struct {
+  const uint32_t* qweight;   /* [N, K/8]                                  */
+  const uint16_t* scales16;  /* fp16 bits [N, K/group]                    */
+  const uint8_t* zeros;      /* [N, K/group], or NULL for symmetric codes */
+} awq_packed;
+size_t w4a16_gated_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t keep);
+awq_status w4a16_gated(const uint16_t* A, int64_t M, int64_t N, int64_t K, int32_t group,
+                       int32_t act, const awq_packed* gate, const awq_packed* up, uint16_t* H,
+                       void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * w4a16_gated_ckpt -- w4a16_gated that also keeps g and u for the backward pass in 8 bits, in
+ * awq_fp8_quantize's format with block_rows 1, cut from the fp32 sums.
+ * g8, u8   out, uint8 [M, N], 16-byte aligned, N % 16 == 0; g_scales, u_scales out, fp32
+ *          [M, ceil(N/128)].
+ * flags    in/out: NONFINITE_ACT (the value's code is NaN).
+ * ws       as w4a16_gated, of w4a16_gated_workspace_bytes(M, N, K, 1) bytes.
+ * Errors: as w4a16_gated; AWQ_ERR_SHAPE also when N % 16 != 0.
+ * ---------------------------------------------------------------------------------------- */
+awq_status w4a16_gated_ckpt(const uint16_t* A, int64_t M, int64_t N, int64_t K, int32_t group,
+                            int32_t act, const awq_packed* gate, const awq_packed* up, uint16_t* H,
+                            uint8_t* g8, float* g_scales, uint8_t* u8, float* u_scales,
+                            uint32_t* flags, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * w4a16_gated_backward -- the gradient of w4a16_gated's input (the packed weights are constants),
+ * from the kept g and u:
+ *   dg = dH u act'(g), du = dH act(g), dA = dg Wg + du Wu.
+ * dH       fp16 bits [M, N]; g8, u8, g_scales, u_scales as w4a16_gated_ckpt leaves them (or
+ *          awq_fp8_quantize; any fp32 scales); dA out, fp16 bits [M, K]. All matrices 16-byte
+ *          aligned, N % 16 == 0.
+ * ws       device workspace, 16-byte aligned, of at least
+ *          w4a16_gated_backward_workspace_bytes(M, N, K, group, zeros given) bytes, any contents:
+ *          dg and du (two fp16 parts each), the steps by column group, fp32 partials. Calls that
+ *          share a workspace must not overlap.
+ * Arithmetic: dg and du in fp32; the products' operands are fp16(d step) (scaled by powers of two
+ * per row and column group) and the exact codes; fp32 sums, in a fixed order; dA rounded once. A
+ * row of dH, g or u that holds an Inf or NaN gives a row of dA that is not finite.
+ * Errors: as w4a16_gated; AWQ_ERR_SHAPE also when N % 16 != 0.
+ * ---------------------------------------------------------------------------------------- */
+size_t w4a16_gated_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t group,
+                                            int32_t zero_point);
+awq_status w4a16_gated_backward(const uint16_t* dH, const uint8_t* g8, const float* g_scales,
+                                const uint8_t* u8, const float* u_scales, int64_t M, int64_t N,
+                                int64_t K, int32_t group, int32_t act, const awq_packed* gate,
+                                const awq_packed* up, uint16_t* dA, void* ws, size_t ws_bytes,
+                                hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * w4a16_gemm_backward -- the gradient of w4a16_gemm's input:
+ *   dA[m,k] = sum_n dY[m,n] c(q[n,k]) scales16[n, k/group] / s16[k]   (s16 NULL: no division).
+ * dY       fp16 bits [M, N] (2-byte aligned; 16-byte aligned rows load faster); dA out, fp16 bits
+ *          [M, K], 16-byte aligned; packed arguments as w4a16_gemm.
+ * ws       as w4a16_gated_backward, of w4a16_gemm_backward_workspace_bytes(M, N, K, group, zeros
+ *          given) bytes. Arithmetic as there.
+ * Errors: AWQ_ERR_NULL, AWQ_ERR_CONFIG, AWQ_ERR_SHAPE (as w4a16_gated), AWQ_ERR_WORKSPACE.
+ * ---------------------------------------------------------------------------------------- */
+size_t w4a16_gemm_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t group,
+                                           int32_t zero_point);
+awq_status w4a16_gemm_backward(const uint16_t* dY, int64_t M, int64_t N, int64_t K, int32_t group,
+                               const uint32_t* qweight, const uint16_t* scales16,
+                               const uint8_t* zeros, const uint16_t* s16, uint16_t* dA, void* ws,
+                               size_t ws_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

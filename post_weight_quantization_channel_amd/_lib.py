@@ -31,6 +31,9 @@ FLAG_STEP_UNDERFLOW = 1 << 7
 FLAG_CLIP_RANGE = 1 << 8
 FLAG_FOLD_RANGE = 1 << 9
 FLAG_NO_GRAM = 1 << 10
+FLAG_NONFINITE_ACT = 1 << 11
+
+AWQ_ACT_SILU, AWQ_ACT_GELU = 0, 1
 
 
 class AwqCfg(ctypes.Structure):
@@ -38,6 +41,11 @@ class AwqCfg(ctypes.Structure):
                 ("n_grid", ctypes.c_int32), ("s_floor", ctypes.c_float), ("form", ctypes.c_int32),
                 ("n_clip", ctypes.c_int32), ("clip_min", ctypes.c_float),
                 ("zero_point", ctypes.c_int32)]
+
+
+class AwqPacked(ctypes.Structure):
+    _fields_ = [("qweight", ctypes.c_void_p), ("scales16", ctypes.c_void_p),
+                ("zeros", ctypes.c_void_p)]
 
 
 _P = ctypes.c_void_p
@@ -80,6 +88,17 @@ SIGNATURES = {
     "awq_act_stats_noalloc": (_E, [_P, _E, _I64, _I64, _I64, _P, _P, _P]),
     "awq_fp8_quantize": (_E, [_P, _E, _I64, _I64, _I64, _I32, _P, _P, _P, _P]),
     "awq_fp8_dequantize": (_E, [_P, _P, _I64, _I64, _I32, _E, _P, _P]),
+    "w4a16_gated_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32]),
+    "w4a16_gated": (_E, [_P, _I64, _I64, _I64, _I32, _I32, ctypes.POINTER(AwqPacked),
+                         ctypes.POINTER(AwqPacked), _P, _P, _SZ, _P]),
+    "w4a16_gated_ckpt": (_E, [_P, _I64, _I64, _I64, _I32, _I32, ctypes.POINTER(AwqPacked),
+                              ctypes.POINTER(AwqPacked), _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "w4a16_gated_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32, _I32]),
+    "w4a16_gated_backward": (_E, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32,
+                                  ctypes.POINTER(AwqPacked), ctypes.POINTER(AwqPacked), _P, _P,
+                                  _SZ, _P]),
+    "w4a16_gemm_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32, _I32]),
+    "w4a16_gemm_backward": (_E, [_P, _I64, _I64, _I64, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "awq_fp8_gemm_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "awq_fp8_gemm": (_E, [_P, _P, _P, _P, _I64, _I64, _I64, _E, _P, _P, _SZ, _P]),
 }

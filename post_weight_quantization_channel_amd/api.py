@@ -568,3 +568,189 @@ def fp8_gemm(A8: torch.Tensor, a_scales: torch.Tensor, W8: torch.Tensor, w_scale
             _DT[out_dtype], out.data_ptr(), ws.data_ptr() if ws is not None else None,
             ws.numel() * ws.element_size() if ws is not None else 0, _stream(A8)))
     return out
+
+
+_ACTS = {"silu": _lib.AWQ_ACT_SILU, "gelu": _lib.AWQ_ACT_GELU}
+
+
+def _packed_check(x, K, qweight, scales16, zeros, group, name):
+    """Checks one packed weight that goes with x on its device; returns N."""
+    _dev(qweight, f"{name} qweight")
+    _dev(scales16, f"{name} scales16")
+    if group not in (64, 128):
+        raise ValueError("group must be 64 or 128")
+    N = qweight.shape[0]
+    if qweight.dtype != torch.int32 or tuple(qweight.shape) != (N, K // 8):
+        raise ValueError(f"{name} qweight must be int32 [N, K/8]")
+    if scales16.dtype != torch.float16 or tuple(scales16.shape) != (N, K // group):
+        raise ValueError(f"{name} scales16 must be fp16 [N, K/group]")
+    if zeros is not None:
+        _dev(zeros, f"{name} zeros")
+        if zeros.dtype != torch.uint8 or tuple(zeros.shape) != (N, K // group):
+            raise ValueError(f"{name} zeros must be uint8 [N, K/group]")
+    _same_device(x, (qweight, f"{name} qweight"), (scales16, f"{name} scales16"),
+                 (zeros, f"{name} zeros"))
+    return N
+
+
+def _packed_arg(qweight, scales16, zeros):
+    return _lib.AwqPacked(qweight.data_ptr(), scales16.data_ptr(),
+                          zeros.data_ptr() if zeros is not None else None)
+
+
+def _gated_check(x, K, gate, up, group, act):
+    N = _packed_check(x, K, *gate, group, "gate")
+    if _packed_check(x, K, *up, group, "up") != N:
+        raise ValueError("gate and up must have the same number of rows")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    if (gate[2] is None) != (up[2] is None):
+        raise ValueError("zeros must be given for both gate and up, or for neither")
+    return N
+
+
+def _halves(t, name):
+    _dev(t, name)
+    if t.dim() != 2 or t.dtype != torch.float16:
+        raise ValueError(f"{name} must be fp16 [rows, columns]")
+
+
+def _ws_args(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def w4a16_gated_workspace_bytes(M: int, N: int, K: int, keep: bool = False) -> int:
+    """Bytes of the w4a16_gated (keep: w4a16_gated_ckpt) workspace (0: none needed)."""
+    return int(_lib.load().w4a16_gated_workspace_bytes(M, N, K, int(keep)))
+
+
+def w4a16_gated(A: torch.Tensor, gate_qweight: torch.Tensor, gate_scales16: torch.Tensor,
+                up_qweight: torch.Tensor, up_scales16: torch.Tensor, group: int = 128,
+                act: str = "silu", out: torch.Tensor | None = None,
+                gate_zeros: torch.Tensor | None = None, up_zeros: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """H = act(A Wg^T) * (A Wu^T), fp16 [M, N], on two packed weights (pack_int4's artefacts) whose
+    s is folded into A's producer; act "silu" or "gelu" (tanh form)."""
+    lib = _lib.load()
+    _halves(A, "A")
+    M, K = A.shape
+    gate = (gate_qweight, gate_scales16, gate_zeros)
+    up = (up_qweight, up_scales16, up_zeros)
+    N = _gated_check(A, K, gate, up, group, act)
+    out = _out(out, (M, N), torch.float16, A.device)
+    ws = _scratch(workspace, lib.w4a16_gated_workspace_bytes(M, N, K, 0), A.device)
+    with torch.cuda.device(A.device):
+        check("w4a16_gated", lib.w4a16_gated(
+            A.data_ptr(), M, N, K, group, _ACTS[act], _packed_arg(*gate), _packed_arg(*up),
+            out.data_ptr(), *_ws_args(ws), _stream(A)))
+    return out
+
+
+@dataclasses.dataclass
+class GatedResult:
+    H: torch.Tensor          # fp16 [M, N]
+    g8: torch.Tensor         # float8_e4m3fn [M, N]: A Wg^T
+    g_scales: torch.Tensor   # fp32 [M, ceil(N / 128)]
+    u8: torch.Tensor         # float8_e4m3fn [M, N]: A Wu^T
+    u_scales: torch.Tensor
+    flags: torch.Tensor
+
+
+def w4a16_gated_ckpt(A: torch.Tensor, gate_qweight: torch.Tensor, gate_scales16: torch.Tensor,
+                     up_qweight: torch.Tensor, up_scales16: torch.Tensor, group: int = 128,
+                     act: str = "silu", gate_zeros: torch.Tensor | None = None,
+                     up_zeros: torch.Tensor | None = None, flags: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None) -> GatedResult:
+    """w4a16_gated that also keeps both projections in 8 bits (fp8_quantize's format, blocks of
+    1 x 128) for w4a16_gated_backward; N a multiple of 16."""
+    lib = _lib.load()
+    _halves(A, "A")
+    M, K = A.shape
+    gate = (gate_qweight, gate_scales16, gate_zeros)
+    up = (up_qweight, up_scales16, up_zeros)
+    N = _gated_check(A, K, gate, up, group, act)
+    dev = A.device
+    flags = _flags(dev, flags)
+    _same_device(A, (flags, "flags"))
+    H = torch.empty((M, N), dtype=torch.float16, device=dev)
+    q = torch.empty((2, M, N), dtype=FP8, device=dev)
+    s = torch.empty((2, *_blocks_shape(M, N, 1)), dtype=torch.float32, device=dev)
+    ws = _scratch(workspace, lib.w4a16_gated_workspace_bytes(M, N, K, 1), dev)
+    with torch.cuda.device(dev):
+        check("w4a16_gated_ckpt", lib.w4a16_gated_ckpt(
+            A.data_ptr(), M, N, K, group, _ACTS[act], _packed_arg(*gate), _packed_arg(*up),
+            H.data_ptr(), q[0].data_ptr(), s[0].data_ptr(), q[1].data_ptr(), s[1].data_ptr(),
+            flags.data_ptr(), *_ws_args(ws), _stream(A)))
+    return GatedResult(H, q[0], s[0], q[1], s[1], flags)
+
+
+def w4a16_gated_backward_workspace_bytes(M: int, N: int, K: int, group: int = 128,
+                                         zero_point: bool = False) -> int:
+    return int(_lib.load().w4a16_gated_backward_workspace_bytes(M, N, K, group, int(zero_point)))
+
+
+def w4a16_gated_backward(dH: torch.Tensor, g8: torch.Tensor, g_scales: torch.Tensor,
+                         u8: torch.Tensor, u_scales: torch.Tensor, gate_qweight: torch.Tensor,
+                         gate_scales16: torch.Tensor, up_qweight: torch.Tensor,
+                         up_scales16: torch.Tensor, group: int = 128, act: str = "silu",
+                         out: torch.Tensor | None = None, gate_zeros: torch.Tensor | None = None,
+                         up_zeros: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """dA, fp16 [M, K]: the gradient of w4a16_gated's input from dH and the kept projections
+    (dg = dH u act'(g), du = dH act(g), dA = dg Wg + du Wu); the packed weights are constants."""
+    lib = _lib.load()
+    _halves(dH, "dH")
+    M, N = dH.shape
+    for q, s, nm in ((g8, g_scales, "g8"), (u8, u_scales, "u8")):
+        _fp8_check(q, s, 1, nm)
+        if tuple(q.shape) != (M, N):
+            raise ValueError(f"{nm} must have dH's shape")
+    K = gate_qweight.shape[1] * 8
+    gate = (gate_qweight, gate_scales16, gate_zeros)
+    up = (up_qweight, up_scales16, up_zeros)
+    if _gated_check(dH, K, gate, up, group, act) != N:
+        raise ValueError("the weights' rows must be dH's columns")
+    _same_device(dH, (g8, "g8"), (g_scales, "g_scales"), (u8, "u8"), (u_scales, "u_scales"))
+    out = _out(out, (M, K), torch.float16, dH.device)
+    ws = _scratch(workspace, lib.w4a16_gated_backward_workspace_bytes(
+        M, N, K, group, int(gate_zeros is not None)), dH.device)
+    with torch.cuda.device(dH.device):
+        check("w4a16_gated_backward", lib.w4a16_gated_backward(
+            dH.data_ptr(), g8.data_ptr(), g_scales.data_ptr(), u8.data_ptr(), u_scales.data_ptr(),
+            M, N, K, group, _ACTS[act], _packed_arg(*gate), _packed_arg(*up), out.data_ptr(),
+            *_ws_args(ws), _stream(dH)))
+    return out
+
+
+def w4a16_gemm_backward_workspace_bytes(M: int, N: int, K: int, group: int = 128,
+                                        zero_point: bool = False) -> int:
+    return int(_lib.load().w4a16_gemm_backward_workspace_bytes(M, N, K, group, int(zero_point)))
+
+
+def w4a16_gemm_backward(dY: torch.Tensor, qweight: torch.Tensor, scales16: torch.Tensor,
+                        s16: torch.Tensor | None, group: int = 128,
+                        out: torch.Tensor | None = None, zeros: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """dA = (dY (c(q) * step)) / s, fp16 [M, K]: the gradient of w4a16_gemm's input; s16 = None
+    when s^-1 is folded into A's producer."""
+    lib = _lib.load()
+    _halves(dY, "dY")
+    M, N = dY.shape
+    K = qweight.shape[1] * 8
+    if _packed_check(dY, K, qweight, scales16, zeros, group, "the weight's") != N:
+        raise ValueError("the weight's rows must be dY's columns")
+    if s16 is not None:
+        _dev(s16, "s16")
+        if s16.dtype != torch.float16 or tuple(s16.shape) != (K,):
+            raise ValueError("s16 must be fp16 [K]")
+        _same_device(dY, (s16, "s16"))
+    out = _out(out, (M, K), torch.float16, dY.device)
+    ws = _scratch(workspace, lib.w4a16_gemm_backward_workspace_bytes(
+        M, N, K, group, int(zeros is not None)), dY.device)
+    with torch.cuda.device(dY.device):
+        check("w4a16_gemm_backward", lib.w4a16_gemm_backward(
+            dY.data_ptr(), M, N, K, group, qweight.data_ptr(), scales16.data_ptr(),
+            zeros.data_ptr() if zeros is not None else None,
+            s16.data_ptr() if s16 is not None else None, out.data_ptr(), *_ws_args(ws),
+            _stream(dY)))
+    return out

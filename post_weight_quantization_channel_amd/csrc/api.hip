@@ -642,4 +642,120 @@ awq_status awq_fp8_gemm(const uint8_t* A8, const float* a_scales, const uint8_t*
                                          static_cast<uint16_t*>(Y), ws, stream));
 }
 
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+
+// sizes of a product with packed weights [N, K] and M rows
+bool packed_sizes_ok(int64_t M, int64_t N, int64_t K) {
+  return M >= 1 && N >= 1 && K >= 128 && K % 128 == 0 && M <= kMaxDim && N <= kMaxDim &&
+         K <= kMaxW4A16K && M * N <= (int64_t(1) << 38);
+}
+
+awq_status check_gated(int64_t M, int64_t N, int64_t K, int32_t group, int32_t act,
+                       const awq_packed* gate, const awq_packed* up) {
+  if (!gate || !up || !gate->qweight || !gate->scales16 || !up->qweight || !up->scales16)
+    return AWQ_ERR_NULL;
+  if (group != 128 && group != 64) return AWQ_ERR_CONFIG;
+  if (act != AWQ_ACT_SILU && act != AWQ_ACT_GELU) return AWQ_ERR_CONFIG;
+  if ((gate->zeros == nullptr) != (up->zeros == nullptr)) return AWQ_ERR_CONFIG;
+  if (!packed_sizes_ok(M, N, K) || !aligned16(gate->qweight) || !aligned16(up->qweight) ||
+      !aligned2(gate->scales16) || !aligned2(up->scales16))
+    return AWQ_ERR_SHAPE;
+  return AWQ_OK;
+}
+
+awq::GatedWeights gated_weights(const awq_packed* gate, const awq_packed* up) {
+  return awq::GatedWeights{{gate->qweight, up->qweight},
+                           {gate->scales16, up->scales16},
+                           {gate->zeros, up->zeros}};
+}
+
+// N of the 8-bit activations: rows of whole 16-byte chunks
+bool saved_sizes_ok(int64_t N) { return N % 16 == 0; }
+
+}  // namespace
+
+size_t w4a16_gated_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t keep) {
+  if (!packed_sizes_ok(M, N, K) || (keep && !saved_sizes_ok(N))) return 0;
+  return awq::w4a16_gated_plan(M, N, K, keep != 0).ws_bytes;
+}
+
+awq_status w4a16_gated(const uint16_t* A, int64_t M, int64_t N, int64_t K, int32_t group,
+                       int32_t act, const awq_packed* gate, const awq_packed* up, uint16_t* H,
+                       void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!A || !H) return AWQ_ERR_NULL;
+  const awq_status cs = check_gated(M, N, K, group, act, gate, up);
+  if (cs != AWQ_OK) return cs;
+  if (!aligned16(A) || !aligned16(H)) return AWQ_ERR_SHAPE;
+  const size_t need = awq::w4a16_gated_plan(M, N, K, false).ws_bytes;
+  if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws))) return AWQ_ERR_WORKSPACE;
+  return hip_status(awq::launch_w4a16_gated(A, M, N, K, group, act, gated_weights(gate, up), H,
+                                            nullptr, nullptr, nullptr, nullptr, nullptr, ws,
+                                            stream));
+}
+
+awq_status w4a16_gated_ckpt(const uint16_t* A, int64_t M, int64_t N, int64_t K, int32_t group,
+                            int32_t act, const awq_packed* gate, const awq_packed* up, uint16_t* H,
+                            uint8_t* g8, float* g_scales, uint8_t* u8, float* u_scales,
+                            uint32_t* flags, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!A || !H || !g8 || !g_scales || !u8 || !u_scales || !flags) return AWQ_ERR_NULL;
+  const awq_status cs = check_gated(M, N, K, group, act, gate, up);
+  if (cs != AWQ_OK) return cs;
+  if (!saved_sizes_ok(N) || !aligned16(A) || !aligned16(H) || !aligned16(g8) || !aligned16(u8) ||
+      !aligned4(g_scales) || !aligned4(u_scales))
+    return AWQ_ERR_SHAPE;
+  const size_t need = awq::w4a16_gated_plan(M, N, K, true).ws_bytes;
+  if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws))) return AWQ_ERR_WORKSPACE;
+  return hip_status(awq::launch_w4a16_gated(A, M, N, K, group, act, gated_weights(gate, up), H, g8,
+                                            g_scales, u8, u_scales, flags, ws, stream));
+}
+
+size_t w4a16_gated_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t group,
+                                            int32_t zero_point) {
+  if (!packed_sizes_ok(M, N, K) || !saved_sizes_ok(N) || (group != 128 && group != 64)) return 0;
+  return awq::w4a16_grad_plan(M, N, K, group, true, zero_point != 0).ws_bytes;
+}
+
+awq_status w4a16_gated_backward(const uint16_t* dH, const uint8_t* g8, const float* g_scales,
+                                const uint8_t* u8, const float* u_scales, int64_t M, int64_t N,
+                                int64_t K, int32_t group, int32_t act, const awq_packed* gate,
+                                const awq_packed* up, uint16_t* dA, void* ws, size_t ws_bytes,
+                                hipStream_t stream) {
+  if (!dH || !g8 || !g_scales || !u8 || !u_scales || !dA) return AWQ_ERR_NULL;
+  const awq_status cs = check_gated(M, N, K, group, act, gate, up);
+  if (cs != AWQ_OK) return cs;
+  if (!saved_sizes_ok(N) || !aligned16(dH) || !aligned16(g8) || !aligned16(u8) || !aligned16(dA) ||
+      !aligned4(g_scales) || !aligned4(u_scales))
+    return AWQ_ERR_SHAPE;
+  const size_t need =
+      awq::w4a16_grad_plan(M, N, K, group, true, gate->zeros != nullptr).ws_bytes;
+  if (!ws || ws_bytes < need || !aligned16(ws)) return AWQ_ERR_WORKSPACE;
+  return hip_status(awq::launch_w4a16_gated_backward(dH, g8, g_scales, u8, u_scales,
+                                                     gated_weights(gate, up), M, N, K, group, act,
+                                                     dA, ws, stream));
+}
+
+size_t w4a16_gemm_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t group,
+                                           int32_t zero_point) {
+  if (!packed_sizes_ok(M, N, K) || (group != 128 && group != 64)) return 0;
+  return awq::w4a16_grad_plan(M, N, K, group, false, zero_point != 0).ws_bytes;
+}
+
+awq_status w4a16_gemm_backward(const uint16_t* dY, int64_t M, int64_t N, int64_t K, int32_t group,
+                               const uint32_t* qweight, const uint16_t* scales16,
+                               const uint8_t* zeros, const uint16_t* s16, uint16_t* dA, void* ws,
+                               size_t ws_bytes, hipStream_t stream) {
+  if (!dY || !qweight || !scales16 || !dA) return AWQ_ERR_NULL;
+  if (group != 128 && group != 64) return AWQ_ERR_CONFIG;
+  if (!packed_sizes_ok(M, N, K) || !aligned2(dY) || !aligned16(qweight) || !aligned2(scales16) ||
+      !aligned16(dA) || (s16 && !aligned2(s16)))
+    return AWQ_ERR_SHAPE;
+  const size_t need = awq::w4a16_grad_plan(M, N, K, group, false, zeros != nullptr).ws_bytes;
+  if (!ws || ws_bytes < need || !aligned16(ws)) return AWQ_ERR_WORKSPACE;
+  return hip_status(awq::launch_w4a16_gemm_backward(dY, qweight, scales16, zeros, s16, M, N, K,
+                                                    group, dA, ws, stream));
+}
+
 }  // extern "C"

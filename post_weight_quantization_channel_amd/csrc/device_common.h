@@ -34,6 +34,7 @@ enum : uint32_t {
   kFlagClipRange = 1u << 8,
   kFlagFoldRange = 1u << 9,
   kFlagNoGram = 1u << 10,
+  kFlagNonfiniteAct = 1u << 11,
 };
 
 __device__ __forceinline__ float h2f(uint16_t b) {

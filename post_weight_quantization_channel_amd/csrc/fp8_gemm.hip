@@ -21,6 +21,7 @@
 // and Y is rounded once.
 #include "fp8_format.h"
 #include "kernels.h"
+#include "tile_order.h"
 
 namespace awq {
 
@@ -142,7 +143,7 @@ template <int BM, int BN, int WM, int WN, int DT>
 __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ sa, const uint8_t* __restrict__ W,
     const float* __restrict__ sw, int64_t M, int64_t N, int64_t K, uint16_t* __restrict__ Y,
-    uint32_t tiles, uint32_t tilesM, uint32_t tilesN, int steps_per_slice,
+    uint32_t tilesM, uint32_t tilesN, int steps_per_slice,
     float* __restrict__ partials, int64_t slice_stride) {
   constexpr int kWaves = WM * WN;
   constexpr int kStage = (BM + BN) * 128;
@@ -155,17 +156,10 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
   const int wm = wave / WN, wn = wave % WN;
   const int li = lane & 15, lg = lane >> 4;
 
-  // workgroup -> tile: each XCD (blockIdx % 8) takes a run of consecutive tiles, ordered in bands
-  // of 8 row tiles so that the 32 tiles an XCD works on together read 8 x 4 operand panels
-  const uint32_t xcd = blockIdx.x & 7u, per = gridDim.x >> 3, rem = gridDim.x & 7u;
-  const uint32_t id = xcd * per + (xcd < rem ? xcd : rem) + (blockIdx.x >> 3);
-  const uint32_t slice = id / tiles, tile = id - slice * tiles;
-  const uint32_t band = tile / (8u * tilesN), in_band = tile - band * 8u * tilesN;
-  const uint32_t bh = tilesM - band * 8u < 8u ? tilesM - band * 8u : 8u;
-  const int64_t m0 = (int64_t)(band * 8u + in_band % bh) * BM;
-  const int64_t n0 = (int64_t)(in_band / bh) * BN;
+  const TileAt at = tile_order<8>(tilesM, tilesN);
+  const int64_t m0 = (int64_t)at.tm * BM, n0 = (int64_t)at.tn * BN;
   const int KB = (int)((K + 127) / 128);
-  const int b0 = (int)slice * steps_per_slice;
+  const int b0 = (int)at.slice * steps_per_slice;
   const int b1 = b0 + steps_per_slice < KB ? b0 + steps_per_slice : KB;
 
   // ---- loads: LDS rows 0 .. BM - 1 are activation rows, BM .. BM + BN - 1 weight rows; load j of
@@ -271,7 +265,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     for (int j = 0; j < NB; ++j) {
       const int64_t n = nw + j * 16 + 4 * lg;
       if (partials) {
-        float* P = partials + (int64_t)slice * slice_stride + m * N + n;
+        float* P = partials + (int64_t)at.slice * slice_stride + m * N + n;
         if (n + 3 < N && (N & 3) == 0) {
           *reinterpret_cast<floatx4*>(P) = acc[i][j];
         } else {
@@ -347,10 +341,10 @@ static hipError_t fp8_gemm_dt(const uint8_t* A, const float* sa, const uint8_t* 
   float* P = p.S > 1 ? static_cast<float*>(ws) : nullptr;
   if (p.tile == 256)
     fp8_tiled_kernel<256, 256, 2, 4, DT><<<tiles * (unsigned)p.S, 512, 2 * 512 * 128, stream>>>(
-        A, sa, W, sw, M, N, K, Y, tiles, tm, tn, (int)p.steps, P, p.stride);
+        A, sa, W, sw, M, N, K, Y, tm, tn, (int)p.steps, P, p.stride);
   else
     fp8_tiled_kernel<128, 128, 2, 2, DT><<<tiles * (unsigned)p.S, 256, 2 * 256 * 128, stream>>>(
-        A, sa, W, sw, M, N, K, Y, tiles, tm, tn, (int)p.steps, P, p.stride);
+        A, sa, W, sw, M, N, K, Y, tm, tn, (int)p.steps, P, p.stride);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.S == 1) return e;
   const int64_t MN = M * N;

@@ -213,4 +213,43 @@ hipError_t launch_fp8_gemm(const uint8_t* A, const float* sa, const uint8_t* W, 
                            int64_t M, int64_t N, int64_t K, int dtype, uint16_t* Y, void* ws,
                            hipStream_t stream);
 
+// ---- the gated feed-forward block on packed weights (w4a16_gated.hip) ----
+// index 0: gate, 1: up; z nullptr for symmetric codes
+struct GatedWeights {
+  const uint32_t* q[2];
+  const uint16_t* s[2];
+  const uint8_t* z[2];
+};
+struct GatedPlan {   // of the tiled kernel
+  int64_t tm, tn;    // tiles
+  int64_t S, steps;  // K slices, 128-channel steps per slice
+  int64_t Np;        // columns of the partials (whole tiles)
+  size_t ws_bytes;   // 0 when S == 1
+};
+GatedPlan w4a16_gated_plan(int64_t M, int64_t N, int64_t K, bool ckpt);
+// g8 nullptr: H only; otherwise g8, u8 [M, N] and gs, us [M, ceil(N / 128)] too (N % 16 == 0)
+hipError_t launch_w4a16_gated(const uint16_t* A, int64_t M, int64_t N, int64_t K, int group,
+                              int act, const GatedWeights& W, uint16_t* H, uint8_t* g8, float* gs,
+                              uint8_t* u8, float* us, uint32_t* flags, void* ws,
+                              hipStream_t stream);
+
+// ---- gradients through packed weights (w4a16_grad.hip) ----
+struct GradPlan {
+  int64_t Nc, C;     // channels of one matrix (rounded up to 32), of the whole contraction
+  int bm;            // tile rows
+  int64_t tm, tk;    // tiles
+  int64_t S, steps;  // slices of the contraction, 32-channel steps per slice
+  size_t off_st, off_sub, off_pmax, off_col, off_unscale, off_hi, off_lo, off_part;
+  size_t ws_bytes;
+};
+GradPlan w4a16_grad_plan(int64_t M, int64_t N, int64_t K, int group, bool gated, bool zp);
+hipError_t launch_w4a16_gemm_backward(const uint16_t* dY, const uint32_t* qweight,
+                                      const uint16_t* scales16, const uint8_t* zeros,
+                                      const uint16_t* s16, int64_t M, int64_t N, int64_t K,
+                                      int group, uint16_t* dA, void* ws, hipStream_t stream);
+hipError_t launch_w4a16_gated_backward(const uint16_t* dH, const uint8_t* g8, const float* gs,
+                                       const uint8_t* u8, const float* us, const GatedWeights& W,
+                                       int64_t M, int64_t N, int64_t K, int group, int act,
+                                       uint16_t* dA, void* ws, hipStream_t stream);
+
 }  // namespace awq

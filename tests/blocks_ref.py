@@ -86,3 +86,62 @@ def act(g, name):
         c = 2 * np.sqrt(2 / np.pi)
         p = 1 / (1 + np.exp(-c * (g + 0.044715 * g ** 3)))
         return g * p, p + g * p * (1 - p) * c * (1 + 3 * 0.044715 * g * g)
+
+
+# ---- the gated block and the gradients ---------------------------------------------------------
+# Bounds. (1) A sum of T exact products in fp32, in any order and grouping, each addition within
+# 2^-23 of the sum of magnitudes (fp16 MFMA and dot instructions cut or round at fp32's last bit),
+# plus the fma by the step of each group: (T + 2 groups + 16) 2^-23 sum |.|; 16 covers the additions
+# of waves and slices. (2) act: p = 1 / (1 + exp2(-z log2 e)) has a relative error of at most
+# (4 |z| + 8) 2^-23: the exponent's product and z itself round by 4 2^-24 |z| at most, exp2, the
+# addition and the reciprocal by an ulp (2^-23) each.
+def sum_slack(terms, groups, magnitudes):
+    return (terms + 2 * groups + 16) * 2.0 ** -23 * magnitudes
+
+
+def act_z(g, name):
+    return np.abs(g) if name == "silu" else 1.6 * (np.abs(g) + 0.0448 * np.abs(g) ** 3)
+
+
+def gated(a, gate, up, group, name):
+    """(g, u, their slack, H, its slack) for a (float64) and unpack()ed weights."""
+    out = []
+    for c, step in (gate, up):
+        mag = np.abs(a) @ np.abs(c * step).T
+        out += [a @ (c * step).T, sum_slack(a.shape[1], a.shape[1] // group, mag)]
+    g, eg, u, eu = out
+    f, _ = act(g, name)
+    ef = 1.2 * eg + np.abs(f) * (4 * act_z(g, name) + 8) * 2.0 ** -23      # |act'| < 1.2
+    return g, eg, u, eu, f * u, ef * (np.abs(u) + eu) + np.abs(f) * eu + 2.0 ** -23 * np.abs(f * u)
+
+
+def grads(dh, g, u, name):
+    """(dg, du, and a bound of their fp32 errors): four products and the activation's errors."""
+    f, df = act(g, name)
+    dg, du = dh * u * df, dh * f
+    rel = (4 * act_z(g, name) + 16) * 2.0 ** -23
+    # df = p + q z', |p|, |q z'| < 1.2 each: its error is relative to those, not to their sum
+    slope = 1.0 if name == "silu" else 1.6 * (1 + 0.1342 * g * g)
+    p = np.where(np.abs(g) > 0, f / np.where(g == 0, 1, g), 0.5)
+    parts = np.abs(p) + np.abs(f * (1 - p)) * slope
+    return dg, du, np.abs(dh * u) * parts * rel + 2.0 ** -22 * np.abs(dg), np.abs(du) * (rel + 2.0 ** -22)
+
+
+def backward(pairs, group):
+    """sum over (d, error of d, (codes, steps)) of d @ (codes * steps), and its slack: each operand
+    fp16(d step) rounds by 2^-11, or by 2^-25 in units of 2^-14 max|d| (the row) times twice the
+    largest step of the column's group (subnormals, of the high and of the low part); then the
+    fp32 sum."""
+    out, slack, mag = 0.0, 0.0, 0.0
+    top_d = np.max([np.abs(d).max(1) for d, _, _ in pairs], 0)
+    top_s = np.max([s.max(0) for _, _, (_, s) in pairs], 0)
+    terms = 0
+    for d, ed, (c, s) in pairs:
+        w = c * s
+        m = np.abs(d) @ np.abs(w)
+        out = out + d @ w
+        mag = mag + m
+        slack = slack + 2.0 ** -11 * m + (1 + 2.0 ** -10) * (ed @ np.abs(w)) + \
+            2 * 2.0 ** -38 * np.outer(top_d, top_s * np.abs(c).sum(0))
+        terms += d.shape[1]
+    return out, slack + sum_slack(terms, 0, mag * (1 + 2.0 ** -10))
