@@ -453,6 +453,24 @@ __device__ __forceinline__ void buffer_load16_lds_so(rsrc_t r, uint32_t lds, uin
       : "memory");
 }
 
+// 4 bytes per lane (offset voff + soff) into LDS: lane l writes bytes [4 l, 4 l + 4) at `lds`, so
+// a wave gathers 64 scattered words into 256 contiguous bytes. Otherwise as buffer_load16_lds_so.
+__device__ __forceinline__ void buffer_load4_lds(rsrc_t r, uint32_t lds, uint32_t voff,
+                                                 uint32_t soff) {
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds);
+  const uint32_t so = __builtin_amdgcn_readfirstlane(soff);
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dword %2, %3, %4 offen lds\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(m0), "v"(voff), "s"(r), "s"(so)
+      : "memory");
+}
+
 // s_waitcnt immediate: at most n vector-memory loads outstanding (gfx9 encoding: vmcnt in bits
 // [3:0] and [15:14]; expcnt and lgkmcnt left at their maxima)
 constexpr int vmcnt_imm(int n) { return (n & 0xF) | ((n >> 4) << 14) | 0x0F70; }

@@ -138,7 +138,8 @@ __global__ __launch_bounds__(64 * kSkWaves) void fp8_skinny_kernel(
 // while the other stage is multiplied: step b waits for its own loads, passes a barrier (everyone's
 // have landed, and the other stage's last reader is done), issues step b + 1's and computes.
 // Chunk c (16 bytes) of LDS row r sits at position c ^ ((r >> 1) & 7): the 16 rows a fragment read
-// touches at once then cover all 64 banks. Rows past M or N, and channels past K, read as zeros.
+// touches at once then cover all 64 banks. The step's activation scales (one per row, gathered)
+// go to LDS the same way. Rows past M or N, and channels past K, read as zeros.
 template <int BM, int BN, int WM, int WN, int DT>
 __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     const uint8_t* __restrict__ A, const float* __restrict__ sa, const uint8_t* __restrict__ W,
@@ -146,7 +147,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     uint32_t tilesM, uint32_t tilesN, int steps_per_slice,
     float* __restrict__ partials, int64_t slice_stride) {
   constexpr int kWaves = WM * WN;
-  constexpr int kStage = (BM + BN) * 128;
+  constexpr int kTiles = (BM + BN) * 128, kStage = kTiles + 4 * BM;
   constexpr int MB = BM / WM / 16, NB = BN / WN / 16;   // 16 x 16 blocks of a wave
   constexpr int kLoads = (BM + BN) / 8 / kWaves;        // 1 KiB loads per wave and step
   static_assert(kLoads % 2 == 0 && (BM / 8) % kLoads == 0, "even, and whole waves per operand");
@@ -187,24 +188,17 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     }
   };
 
-  // ---- scales: sa of the lane's activation rows (clamped to M - 1), sw of the wave's columns ---
-  const float* sar[MB];
-#pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int64_t m = m0 + (wm * MB + i) * 16 + li;
-    sar[i] = sa + (m < M ? m : M - 1) * KB;
-  }
+  // ---- scales: wave w < BM / 64 gathers sa of rows 64 w .. 64 w + 63; sw is one value per wave ----
+  const rsrc_t rs = make_rsrc(sa + m0 * KB, (uint32_t)((M - m0 < BM ? M - m0 : BM) * KB * 4));
+  const uint32_t soff = (uint32_t)(64 * wave + lane) * (uint32_t)KB * 4u;
+  auto issue_scales = [&](int b, int st) {
+    if (wave < BM / 64)
+      buffer_load4_lds(rs, lds0 + (uint32_t)(st * kStage + kTiles + 256 * wave), soff,
+                       (uint32_t)b * 4u);
+  };
   const int64_t nw = n0 + wn * NB * 16;             // the wave's first column
   const float* swr = sw + ((nw < N ? nw : N - 1) >> 7) * KB;
   static_assert(BN / WN <= 128 && 128 % (BN / WN) == 0, "one weight scale per wave and step");
-  struct Scales {
-    float a[MB], w;
-  };
-  auto load_scales = [&](int b, Scales& s) {
-#pragma unroll
-    for (int i = 0; i < MB; ++i) s.a[i] = sar[i][b];
-    s.w = swr[b];
-  };
 
   // ---- fragments: row r at r * 128, chunks lg and lg + 4 --------------------------------------
   const int key = (li >> 1) & 7;
@@ -219,8 +213,9 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
   for (int i = 0; i < MB; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
-  auto compute = [&](int st, const Scales& s) {
+  auto compute = [&](int st, float swv) {
     const char* base = smem + st * kStage;
+    const float* srow = reinterpret_cast<const float*>(base + kTiles) + wm * MB * 16 + li;
     const char* arow = base + wm * MB * 16 * 128;
     const char* wrow = base + (BM + wn * NB * 16) * 128;
     intx8 wf[NB];
@@ -229,7 +224,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
       const intx8 af = frag(arow + i * 16 * 128);
-      const float sc = s.a[i] * s.w;
+      const float sc = srow[i * 16] * swv;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         const floatx4 p = mfma_fp8(wf[j], af, floatx4{0.f, 0.f, 0.f, 0.f});
@@ -239,21 +234,20 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
     }
   };
 
-  Scales sc[2];
   issue(b0, 0);
-  load_scales(b0, sc[0]);
-  auto step = [&](int b, int st, const Scales& cur, Scales& nxt) {
+  issue_scales(b0, 0);
+  float swv = swr[b0];
+  for (int b = b0; b < b1; ++b) {
+    const int st = (b - b0) & 1;
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     __syncthreads();
+    const float swn = swr[b + 1 < b1 ? b + 1 : b];
     if (b + 1 < b1) {
       issue(b + 1, st ^ 1);
-      load_scales(b + 1, nxt);
+      issue_scales(b + 1, st ^ 1);
     }
-    compute(st, cur);
-  };
-  for (int b = b0; b < b1; b += 2) {
-    step(b, 0, sc[0], sc[1]);
-    if (b + 1 < b1) step(b + 1, 1, sc[1], sc[0]);
+    compute(st, swv);
+    swv = swn;
   }
 
   // ---- store ----------------------------------------------------------------------------------
@@ -340,10 +334,10 @@ static hipError_t fp8_gemm_dt(const uint8_t* A, const float* sa, const uint8_t* 
   const uint32_t tiles = tm * tn;
   float* P = p.S > 1 ? static_cast<float*>(ws) : nullptr;
   if (p.tile == 256)
-    fp8_tiled_kernel<256, 256, 2, 4, DT><<<tiles * (unsigned)p.S, 512, 2 * 512 * 128, stream>>>(
+    fp8_tiled_kernel<256, 256, 2, 4, DT><<<tiles * (unsigned)p.S, 512, 2 * (512 * 128 + 1024), stream>>>(
         A, sa, W, sw, M, N, K, Y, tm, tn, (int)p.steps, P, p.stride);
   else
-    fp8_tiled_kernel<128, 128, 2, 2, DT><<<tiles * (unsigned)p.S, 256, 2 * 256 * 128, stream>>>(
+    fp8_tiled_kernel<128, 128, 2, 2, DT><<<tiles * (unsigned)p.S, 256, 2 * (256 * 128 + 512), stream>>>(
         A, sa, W, sw, M, N, K, Y, tm, tn, (int)p.steps, P, p.stride);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.S == 1) return e;
