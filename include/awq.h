@@ -473,7 +473,8 @@ awq_status awq_fp8_gemm(const uint8_t* A8, const float* a_scales, const uint8_t*
  * folded into the operator that produces it (awq_search_layers, awq_fold_scale): A comes divided.
  * A        fp16 bits [M, K]; H out, fp16 bits [M, N]; both 16-byte aligned.
  * gate, up host structs (read during the call) of device pointers, as w4a16_gemm's arguments:
- *          both with zeros, or both without.
+ *          both with zeros, or both without. With groups of 64, scales16 4-byte and zeros 2-byte
+ *          aligned.
  * act      AWQ_ACT_SILU: g / (1 + exp(-g)); AWQ_ACT_GELU: 0.5 g (1 + tanh(sqrt(2/pi) (g +
  *          0.044715 g^3))).
  * ws       device workspace, 16-byte aligned, of at least w4a16_gated_workspace_bytes(M, N, K, 0)

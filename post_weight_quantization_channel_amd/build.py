@@ -13,9 +13,9 @@ post_weight_quantization_channel_amd/libawq.so. Arithmetic flags:
                                         no packed fp32 (v_pk_*_f32) instructions
 Denormals are left enabled (no -fgpu-flush-denormals-to-zero), no fast-math.
 Per-source additions (FILE_FLAGS):
-  w4a16.hip: -mllvm -amdgpu-mfma-vgpr-form
-                                        MFMA results in VGPRs: the tiled kernel scales every
-                                        group's partial sums with vector instructions, which would
+  w4a16.hip, w4a16_gated.hip, fp8_gemm.hip: -mllvm -amdgpu-mfma-vgpr-form
+                                        MFMA results in VGPRs: the tiled kernels scale every
+                                        group's sums with vector instructions, which would
                                         otherwise first copy them out of AGPRs
 """
 from __future__ import annotations
@@ -44,6 +44,8 @@ FLAGS = [
 
 FILE_FLAGS = {
     "w4a16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "w4a16_gated.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "fp8_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
 

@@ -663,6 +663,10 @@ awq_status check_gated(int64_t M, int64_t N, int64_t K, int32_t group, int32_t a
   if (!packed_sizes_ok(M, N, K) || !aligned16(gate->qweight) || !aligned16(up->qweight) ||
       !aligned2(gate->scales16) || !aligned2(up->scales16))
     return AWQ_ERR_SHAPE;
+  // groups of 64: both groups of a 128-channel step are read at once
+  if (group == 64 && (!aligned4(gate->scales16) || !aligned4(up->scales16) ||
+                      !aligned2(gate->zeros) || !aligned2(up->zeros)))
+    return AWQ_ERR_SHAPE;
   return AWQ_OK;
 }
 

@@ -221,6 +221,7 @@ struct GatedWeights {
   const uint8_t* z[2];
 };
 struct GatedPlan {   // of the tiled kernel
+  int bm;            // rows of a tile
   int64_t tm, tn;    // tiles
   int64_t S, steps;  // K slices, 128-channel steps per slice
   int64_t Np;        // columns of the partials (whole tiles)

@@ -10,8 +10,8 @@
 //   M <= 2    w4a16_gated_gemv_kernel: bound by the codes' bytes; a wave owns one output channel,
 //             its gate row and its up row.
 //   M <= 32   w4a16_gated_skinny_kernel: MFMA, codes from memory to registers, K over 8 waves.
-//   else      w4a16_gated_tiled_kernel: 64 rows x 128 output channels; with few tiles K is split
-//             over workgroups and w4a16_gated_finish_kernel adds the slices in order and applies
+//   else      w4a16_gated_tiled_kernel: 128 (or 64) rows x 128 output channels; with few tiles K is
+//             split over workgroups and w4a16_gated_finish_kernel adds the slices in order and applies
 //             the activation. The 8-bit form always takes this path: 128 output channels of a
 //             tile are one block of the format.
 #include "fp8_format.h"
@@ -26,7 +26,7 @@ constexpr int kGvPos = 2;         // chunk positions per lane whose loads are in
 constexpr int kChunkBytes = 80;   // LDS bytes per 32-channel chunk: 64 of activations, 16 padding
 constexpr int kGvWaves = 8;
 constexpr int kSkWaves = 8;
-constexpr int kTM = 64, kTN = 128;   // tile of the tiled kernel: rows, output channels
+constexpr int kTN = 128;          // output channels of a tile of the tiled kernel
 }  // namespace
 
 // ---------------------------------------------------------------------------------------------
@@ -183,9 +183,10 @@ namespace {
 // The fragment of one word of 8 codes: exact fp16 values in natural order. Byte j of the word
 // (channels 2j, 2j + 1) is spread to bytes 0 and 2; with the exponent bits around them the pair is
 // (1024 + u, 1024 + 16 u'), and one packed fma with (1, 1/16) and -(1024 + zc, 64 + zc) gives
-// (c, c'); zc = 8 for signed codes (biased by the xor) or the zero point.
+// (c, c'); zc = 8 for signed codes (biased by the xor) or the zero point. mul = (1, 1/16); with
+// mul and nsub zero the values are zero.
 template <bool ZP>
-__device__ __forceinline__ half8_t decode8(uint32_t w, uint32_t magic, half2_t nsub) {
+__device__ __forceinline__ half8_t decode8(uint32_t w, uint32_t magic, half2_t mul, half2_t nsub) {
   const uint32_t x = ZP ? w : (w ^ 0x88888888u);
   half8_t f;
 #pragma unroll
@@ -193,7 +194,7 @@ __device__ __forceinline__ half8_t decode8(uint32_t w, uint32_t magic, half2_t n
     const uint32_t t = __builtin_amdgcn_perm(x, x, 0x0C000C00u | (uint32_t)j | ((uint32_t)j << 16));
     const uint32_t bits = (t & 0x00F0000Fu) | magic;
     const half2_t q = __builtin_elementwise_fma(
-        __builtin_bit_cast(half2_t, bits), half2_t{(_Float16)1.0f, (_Float16)0.0625f}, nsub);
+        __builtin_bit_cast(half2_t, bits), mul, nsub);
     f[2 * j] = q[0];
     f[2 * j + 1] = q[1];
   }
@@ -285,7 +286,8 @@ __global__ __launch_bounds__(64 * kSkWaves) void w4a16_gated_skinny_kernel(
         for (int t = 0; t < MT; ++t) part[t] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kk = h * 4 / kG; kk < (h + 1) * 4 / kG; ++kk) {
-          const half8_t wf = decode8<ZP>(b.w[r][kk], magic, nsub);
+          const half8_t wf = decode8<ZP>(b.w[r][kk], magic,
+                                         half2_t{(_Float16)1.0f, (_Float16)0.0625f}, nsub);
 #pragma unroll
           for (int t = 0; t < MT; ++t)
             part[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b.a[t][kk], wf, part[t], 0, 0, 0);
@@ -332,12 +334,18 @@ __global__ __launch_bounds__(64 * kSkWaves) void w4a16_gated_skinny_kernel(
 }
 
 // ---------------------------------------------------------------------------------------------
-// Tile of 64 rows x 128 output channels, 128 channels of K per step, 4 waves; wave w owns the
-// output channels 32 w .. 32 w + 31 (their gate and up rows: four 16-column blocks) for all 64
-// rows, so every code is decoded once per tile. The activation tile (64 rows of 256 bytes) is
+// Tile of TM rows x 128 output channels, 128 channels of K per step, 4 waves; wave w owns the
+// output channels 32 w .. 32 w + 31 (their gate and up rows: four 16-column blocks) for all TM
+// rows, so every code is decoded once per tile. The activation tile (TM rows of 256 bytes) is
 // moved into one of two LDS stages by the buffer unit, chunk c of row r at position c ^ (r & 15);
 // each wave loads its codes, steps and zero points into registers one step ahead. Step b waits
 // for its loads, passes a barrier, issues step b + 1's loads and computes.
+//
+// The steps change with the group, so they cannot be left to the end; instead of a second set of
+// registers for the group's partial sums, the accumulators hold sum / (the current group's step):
+// at a group's start they are multiplied by (last step / this step), and by the last step at the
+// end. Each such factor is within 2^-22 of the quotient. A group whose step is 0 decodes to zeros
+// and keeps the step before it.
 // Rows past M read as zeros, output channels past N read channel N - 1; neither is stored.
 struct GatedOut {
   uint16_t* H;
@@ -346,101 +354,121 @@ struct GatedOut {
   uint32_t* flags;
 };
 
-template <int GS, bool ZP, int ACT, bool CKPT>
+template <int GS, bool ZP, int ACT, bool CKPT, int TM>
 __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
     const uint16_t* __restrict__ A, int64_t M, int64_t N, int64_t K, GatedWeights W, GatedOut O,
     uint32_t tilesM, uint32_t tilesN, int steps_per_slice, float* __restrict__ partials,
     int64_t Np) {
   constexpr int kG = 128 / GS;
-  constexpr int kStage = kTM * 256;
+  constexpr int kStage = TM * 256;
+  constexpr int MB = TM / 16;
   __shared__ __attribute__((aligned(1024))) char smem[2 * kStage];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 15, lg = lane >> 4;
   const TileAt at = tile_order<8>(tilesM, tilesN);
-  const int64_t m0 = (int64_t)at.tm * kTM, n0 = (int64_t)at.tn * kTN;
+  const int64_t m0 = (int64_t)at.tm * TM, n0 = (int64_t)at.tn * kTN;
   const int KB = (int)(K / 128);
   const int b0 = (int)at.slice * steps_per_slice;
   const int b1 = b0 + steps_per_slice < KB ? b0 + steps_per_slice : KB;
 
-  const rsrc_t ra = make_rsrc(A + m0 * K, (uint32_t)((M - m0 < kTM ? M - m0 : kTM) * K * 2));
+  const rsrc_t ra = make_rsrc(A + m0 * K, (uint32_t)((M - m0 < TM ? M - m0 : TM) * K * 2));
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(smem));
   uint32_t voff[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)   // load j of wave w: rows 16 w + 4 j + lane / 16
+  for (int j = 0; j < 4; ++j)   // load j of wave w: rows TM / 4 w + 4 j + lane / 16
     voff[j] = (uint32_t)(lg * K * 2) + (uint32_t)((li ^ (4 * j + lg)) << 4);
   auto issue = [&](int b, int st) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r0 = 16 * wave + 4 * j;
-      buffer_load16_lds_so(ra, lds0 + (uint32_t)(st * kStage + r0 * 256), voff[j],
+    for (int j = 0; j < MB; ++j) {
+      const int r0 = TM / 4 * wave + 4 * j;
+      buffer_load16_lds_so(ra, lds0 + (uint32_t)(st * kStage + r0 * 256), voff[j & 3],
                            (uint32_t)(r0 * K * 2) + (uint32_t)b * 256u);
     }
   };
-  // column blocks t = 2 matrix + half: output channels n0 + 32 wave + 16 half + li
-  int64_t nrow[2];
+  // column blocks t = 2 matrix + half: output channels n0 + 32 wave + 16 half + li. Byte offsets
+  // of the lane's rows from the tile's first row (128 rows of at most 16 KiB).
+  const char *qb[2], *sb[2], *zb[2];
+  uint32_t qoff[2], goff[2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t n = n0 + 32 * wave + 16 * h + li;
-    nrow[h] = n < N ? n : N - 1;
+  for (int r = 0; r < 2; ++r) {
+    qb[r] = reinterpret_cast<const char*>(W.q[r] + n0 * (K / 8));
+    sb[r] = reinterpret_cast<const char*>(W.s[r] + n0 * (K / GS));
+    zb[r] = ZP ? reinterpret_cast<const char*>(W.z[r] + n0 * (K / GS)) : nullptr;
+    const int64_t n = 32 * wave + 16 * r + li;
+    const uint32_t row = (uint32_t)(n0 + n < N ? n : N - 1 - n0);
+    qoff[r] = row * (uint32_t)(K / 2) + (uint32_t)lg * (GS == 128 ? 16u : 8u);
+    goff[r] = row * (uint32_t)(K / GS);
   }
   struct Codes {
-    uint32_t w[4][4], st[4][kG], z[4][kG];
+    uint32_t w[4][4], st[4], z[4];   // st, z: groups of 64 hold both groups' values
   };
   auto load_codes = [&](int b, Codes& c) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const int64_t n = nrow[t & 1];
-      load_block<GS>(W.q[t >> 1] + n * (K / 8) + (int64_t)b * 16, lg, c.w[t]);
-#pragma unroll
-      for (int h = 0; h < kG; ++h) {
-        const int64_t g = n * (K / GS) + (int64_t)b * kG + h;
-        c.st[t][h] = W.s[t >> 1][g];
-        if (ZP) c.z[t][h] = W.z[t >> 1][g];
+      const char* q = qb[t >> 1] + (uint32_t)b * 64u;
+      if (GS == 128) {
+        const uint4 v = *reinterpret_cast<const uint4*>(q + qoff[t & 1]);
+        c.w[t][0] = v.x; c.w[t][1] = v.y; c.w[t][2] = v.z; c.w[t][3] = v.w;
+        c.st[t] = *reinterpret_cast<const uint16_t*>(sb[t >> 1] + (uint32_t)b * 2u + 2u * goff[t & 1]);
+        if (ZP) c.z[t] = *reinterpret_cast<const uint8_t*>(zb[t >> 1] + (uint32_t)b + goff[t & 1]);
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(q + qoff[t & 1]);
+        const uint2 x = *reinterpret_cast<const uint2*>(q + qoff[t & 1] + 32);
+        c.w[t][0] = v.x; c.w[t][1] = v.y; c.w[t][2] = x.x; c.w[t][3] = x.y;
+        c.st[t] = *reinterpret_cast<const uint32_t*>(sb[t >> 1] + (uint32_t)b * 4u + 2u * goff[t & 1]);
+        if (ZP)
+          c.z[t] = *reinterpret_cast<const uint16_t*>(zb[t >> 1] + (uint32_t)b * 2u + goff[t & 1]);
       }
     }
   };
   uint32_t magic = 0x64006400u;
   asm volatile("" : "+v"(magic));
-  floatx4 acc[4][4];   // [column block][16-row block]
+  floatx4 acc[4][MB];   // [column block][16-row block]
+  float prev[4];        // the step the accumulators are divided by
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
+  for (int t = 0; t < 4; ++t) {
+    prev[t] = 1.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[t][i] = floatx4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < MB; ++i) acc[t][i] = floatx4{0.f, 0.f, 0.f, 0.f};
+  }
   auto compute = [&](int st, const Codes& c) {
     const char* sa = smem + st * kStage;
 #pragma unroll
     for (int h = 0; h < kG; ++h) {
-      half2_t nsub[4];
+      half2_t nsub[4], mul[4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) nsub[t] = decode_nsub(ZP ? (float)c.z[t][h] : 8.0f);
-      floatx4 part[4][4];
+      for (int t = 0; t < 4; ++t) {
+        const float s = h2f((uint16_t)(h == 0 ? c.st[t] & 0xFFFFu : c.st[t] >> 16));
+        const float z = ZP ? (float)(GS == 128 ? c.z[t] : h == 0 ? c.z[t] & 0xFFu : c.z[t] >> 8) : 8.0f;
+        const bool none = s == 0.0f;
+        const half2_t zero2 = half2_t{(_Float16)0.0f, (_Float16)0.0f};
+        nsub[t] = none ? zero2 : decode_nsub(z);
+        mul[t] = none ? zero2 : half2_t{(_Float16)1.0f, (_Float16)0.0625f};
+        const float now = none ? prev[t] : s;
+        const float ratio = prev[t] * __builtin_amdgcn_rcpf(now);
+        prev[t] = now;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+        for (int i = 0; i < MB; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) part[t][i] = floatx4{0.f, 0.f, 0.f, 0.f};
+          for (int e = 0; e < 4; ++e) acc[t][i][e] *= ratio;
+      }
 #pragma unroll
       for (int kk = h * 4 / kG; kk < (h + 1) * 4 / kG; ++kk) {
         const int ch = chunk_of<GS>(lg, kk);
-        half8_t wf[4], af[4];
+        half8_t wf[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          af[i] = *reinterpret_cast<const half8_t*>(sa + (16 * i + li) * 256 + ((ch ^ li) << 4));
+        for (int t = 0; t < 4; ++t) wf[t] = decode8<ZP>(c.w[t][kk], magic, mul[t], nsub[t]);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) wf[t] = decode8<ZP>(c.w[t][kk], magic, nsub[t]);
+        for (int i = 0; i < MB; ++i) {
+          const half8_t af =
+              *reinterpret_cast<const half8_t*>(sa + (16 * i + li) * 256 + ((ch ^ li) << 4));
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            part[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(af[i], wf[t], part[t][i], 0, 0, 0);
-      }
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const float sc = h2f((uint16_t)c.st[t][h]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[t][i][e] = __builtin_fmaf(part[t][i][e], sc, acc[t][i][e]);
+          for (int t = 0; t < 4; ++t)
+            acc[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(af, wf[t], acc[t][i], 0, 0, 0);
+        }
+        // decoding further ahead would not fit the registers
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   };
@@ -460,6 +488,12 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
     step(b, 0, cb[0], cb[1]);
     if (b + 1 < b1) step(b + 1, 1, cb[1], cb[0]);
   }
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[t][i][e] *= prev[t];
 
   // a lane holds, for block i and element e, row m0 + 16 i + 4 lg + e of its output channels
   if (partials) {   // [slice][matrix][M][Np], Np = whole tiles
@@ -467,7 +501,7 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < MB; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int64_t m = m0 + 16 * i + 4 * lg + e;
@@ -477,13 +511,13 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
     return;
   }
   __syncthreads();   // the last step's reads of the stages are done
-  // H (64 x 256 B), and the codes of g and u (64 x 128 B each), go through LDS to whole-row stores
+  // H (TM x 256 B), and the codes of g and u (TM x 128 B each), go through LDS to whole-row stores
   char* hl = smem;
-  char* cl = smem + kTM * 256;
+  char* cl = smem + TM * 256;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MB; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int row = 16 * i + 4 * lg + e, col = 32 * wave + 16 * h + li;
@@ -491,12 +525,12 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
             f2h(act_f<ACT>(acc[h][i][e]) * acc[2 + h][i][e]);
       }
   if constexpr (CKPT) {
-    __shared__ float wmax[2][4][kTM];
+    __shared__ float wmax[2][4][TM];
     bool any = false;
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < MB; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint32_t mx = 0u;
@@ -515,7 +549,7 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < MB; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int row = 16 * i + 4 * lg + e;
@@ -529,13 +563,13 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
             const float v = acc[2 * r + h][i][e];
             uint32_t code = fp8_pack4(v * s.inv, 0.0f, 0.0f, 0.0f) & 0xFFu;
             if ((__float_as_uint(v) & 0x7FFFFFFFu) >= 0x7F800000u) code = 0x7Fu;
-            cl[r * kTM * 128 + row * 128 + 32 * wave + 16 * h + li] = (char)code;
+            cl[r * TM * 128 + row * 128 + 32 * wave + 16 * h + li] = (char)code;
           }
         }
     wave_flag(O.flags, any, kFlagNonfiniteAct);
   }
   __syncthreads();
-  for (int e = tid; e < kTM * 16; e += 256) {   // 16 bytes of H each
+  for (int e = tid; e < TM * 16; e += 256) {   // 16 bytes of H each
     const int row = e >> 4;
     const int64_t m = m0 + row, n = n0 + 8 * (e & 15);
     if (m >= M || n >= N) continue;
@@ -551,12 +585,12 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
     }
   }
   if constexpr (CKPT) {
-    for (int e = tid; e < 2 * kTM * 8; e += 256) {   // 16 codes each; N % 16 == 0 here
-      const int r = e / (kTM * 8), row = (e >> 3) % kTM;
+    for (int e = tid; e < 2 * TM * 8; e += 256) {   // 16 codes each; N % 16 == 0 here
+      const int r = e / (TM * 8), row = (e >> 3) % TM;
       const int64_t m = m0 + row, n = n0 + 16 * (e & 7);
       if (m < M && n < N)
         *reinterpret_cast<uint4*>((r == 0 ? O.g8 : O.u8) + m * N + n) =
-            *reinterpret_cast<const uint4*>(cl + r * kTM * 128 + row * 128 + (e & 7) * 16);
+            *reinterpret_cast<const uint4*>(cl + r * TM * 128 + row * 128 + (e & 7) * 16);
     }
   }
 }
@@ -625,7 +659,8 @@ GatedPlan w4a16_gated_plan(int64_t M, int64_t N, int64_t K, bool ckpt) {
   GatedPlan p{};
   p.S = 1;
   if (!ckpt && M <= 32) return p;
-  p.tm = (M + kTM - 1) / kTM;
+  p.bm = M > 64 ? 128 : 64;
+  p.tm = (M + p.bm - 1) / p.bm;
   p.tn = (N + kTN - 1) / kTN;
   p.Np = p.tn * kTN;
   const int64_t KB = K / 128, tiles = p.tm * p.tn;
@@ -678,12 +713,15 @@ static hipError_t gated(const uint16_t* A, int64_t M, int64_t N, int64_t K, cons
   const GatedPlan p = w4a16_gated_plan(M, N, K, ckpt);
   float* P = p.S > 1 ? static_cast<float*>(ws) : nullptr;
   const unsigned grid = (unsigned)(p.tm * p.tn * p.S);
-  if (ckpt)
-    w4a16_gated_tiled_kernel<GS, ZP, ACT, true><<<grid, 256, 0, stream>>>(
-        A, M, N, K, W, O, (uint32_t)p.tm, (uint32_t)p.tn, (int)p.steps, P, p.Np);
-  else
-    w4a16_gated_tiled_kernel<GS, ZP, ACT, false><<<grid, 256, 0, stream>>>(
-        A, M, N, K, W, O, (uint32_t)p.tm, (uint32_t)p.tn, (int)p.steps, P, p.Np);
+#define AWQ_GT(CKPT_, TM_)                                                    \
+  w4a16_gated_tiled_kernel<GS, ZP, ACT, CKPT_, TM_><<<grid, 256, 0, stream>>>( \
+      A, M, N, K, W, O, (uint32_t)p.tm, (uint32_t)p.tn, (int)p.steps, P, p.Np)
+  if (p.bm == 128) {
+    if (ckpt) AWQ_GT(true, 128); else AWQ_GT(false, 128);
+  } else {
+    if (ckpt) AWQ_GT(true, 64); else AWQ_GT(false, 64);
+  }
+#undef AWQ_GT
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.S == 1) return e;
   const unsigned fgrid = (unsigned)((M * p.tn + 15) / 16);

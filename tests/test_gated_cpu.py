@@ -49,6 +49,10 @@ def test_gated_refuses(lib):
                                     (5, 2, CONFIG), (5, -1, CONFIG), (0, P + 8, SHAPE),
                                     (8, P + 2, SHAPE)] + sizes(1, 2, 3) +
             [(6, w, s) for w, s in WEIGHTS] + [(7, w, s) for w, s in WEIGHTS])
+    for bad in (pk(s=P + 2), pk(z=P + 1)):       # groups of 64 are read two at a time
+        other = pk(z=P if bad.zeros else None)
+        assert lib.w4a16_gated(P, 4, 64, 256, 64, 0, bad, other, P, P, BIG, None) == SHAPE
+        assert lib.w4a16_gated(P, 4, 64, 256, 64, 0, other, bad, P, P, BIG, None) == SHAPE
     need = lib.w4a16_gated_workspace_bytes(64, 256, 4096, 0)
     assert need > 0
     split = [P, 64, 256, 4096, 128, 0, pk(), pk(), P, P, need - 1, None]
