@@ -393,44 +393,68 @@ __global__ __launch_bounds__(BM == 256 ? 512 : 256) void grad_gemm_kernel(
     }
   };
 
+  // The loads and the writes are unconditional (the last steps load the slice's last step again and
+  // write a stage nobody reads): behind a branch the compiler has to wait for the newest loads
+  // before it uses the older ones (1285 us instead of LOOPTIME for 4096 rows of 2 x 11008 x 4096).
+  const int last = s1 - 1;
   Regs R[2];
   load(s0, R[0]);
-  if (s0 + 1 < s1) load(s0 + 1, R[1]);
+  load(s0 < last ? s0 + 1 : last, R[1]);
   put(0, R[0]);
   // step t (stage t & 1 from s0): registers of step t + 1 are in nxt, cur's are free
   auto step = [&](int t, int stage, Regs& cur, Regs& nxt) {
     __syncthreads();                                 // stage written, other stage read
-    if (t + 2 < s1) load(t + 2, cur);
-    if (t + 1 < s1) put(stage ^ 1, nxt);
+    load(t + 2 < last ? t + 2 : last, cur);
+    put(stage ^ 1, nxt);
     compute(stage);
   };
-  for (int t = s0; t < s1; t += 2) {
+  int t = s0;
+  for (; t + 1 < s1; t += 2) {
     step(t, 0, R[0], R[1]);
-    if (t + 1 < s1) step(t + 1, 1, R[1], R[0]);
+    step(t + 1, 1, R[1], R[0]);
+  }
+  if (t < s1) {
+    __syncthreads();
+    compute(0);
   }
 
   // ---- store: a lane's block j holds column 8 w + i8, w = lane % WPG -------------------------
-  const int w = l32 % WPG;
-#pragma unroll
-  for (int j = 0; j < NBLK; ++j) {
-    const int64_t k = k0 + vg * G + 8 * w + (32 / WPG) * j + l32 / WPG;
-    if (k >= S.K) continue;
-    const float cs = colscale[k / G], sv = s16 ? h2f(s16[k]) : 1.0f;
+  const int64_t kl = k0 + vg * G + 8 * (l32 % WPG) + l32 / WPG;   // of block 0; + 32 / WPG per block
+  const int64_t ml = m0 + mq * RM + 4 * lh;
+  if (kl >= S.K) return;   // a whole group of columns: K % G == 0
+  if (partials) {
+    float* P = partials + (int64_t)at.slice * S.M * S.K + kl;
 #pragma unroll
     for (int i = 0; i < MBLK; ++i)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const int64_t m = m0 + mq * RM + 32 * i + 8 * (e >> 2) + 4 * lh + (e & 3);
-        if (m >= S.M) continue;
-        if (partials) {
-          partials[((int64_t)at.slice * S.M + m) * S.K + k] = acc[i][j][e];
-        } else {
-          float v = acc[i][j][e] * (unscale[m] * cs);
-          if (s16) v = v / sv;
-          dA[m * S.K + k] = f2h(v);
+        const int64_t m = ml + 32 * i + 8 * (e >> 2) + (e & 3);
+        if (m < S.M) {
+#pragma unroll
+          for (int j = 0; j < NBLK; ++j) P[m * S.K + (32 / WPG) * j] = acc[i][j][e];
         }
       }
+    return;
   }
+  const float cs = colscale[kl / G];
+  float sv[NBLK];
+#pragma unroll
+  for (int j = 0; j < NBLK; ++j) sv[j] = s16 ? h2f(s16[kl + (32 / WPG) * j]) : 1.0f;
+#pragma unroll
+  for (int i = 0; i < MBLK; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int64_t m = ml + 32 * i + 8 * (e >> 2) + (e & 3);
+      if (m < S.M) {
+        const float us = unscale[m] * cs;
+#pragma unroll
+        for (int j = 0; j < NBLK; ++j) {
+          float v = acc[i][j][e] * us;
+          if (s16) v = v / sv[j];
+          dA[m * S.K + kl + (32 / WPG) * j] = f2h(v);
+        }
+      }
+    }
 }
 
 // dA = round(sum of the slices' partials [slices][M][K] times 2^(f - e) (/ s[k])), slices in order.
