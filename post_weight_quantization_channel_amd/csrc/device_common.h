@@ -404,6 +404,19 @@ __device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t num_bytes
   return r;
 }
 
+// Plain loads through such a descriptor (16 and 4 bytes at byte offset voff; zeros past its range).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(rsrc_t r) {
+  const uint64_t base = (uint64_t)(uint32_t)r[0] | ((uint64_t)(uint32_t)r[1] << 32);
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, r[2], r[3]);
+}
+__device__ __forceinline__ uint4 buffer_load16(rsrc_t r, uint32_t voff) {
+  const auto v = __builtin_amdgcn_raw_buffer_load_b128(buffer_of(r), (int)voff, 0, 0);
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ uint32_t buffer_load4(rsrc_t r, uint32_t voff) {
+  return __builtin_amdgcn_raw_buffer_load_b32(buffer_of(r), (int)voff, 0, 0);
+}
+
 // LDS byte address of a __shared__ object (for M0 below).
 typedef __attribute__((address_space(3))) char lds_char_t;
 __device__ __forceinline__ uint32_t lds_addr(const void* shared_obj) {

@@ -247,117 +247,118 @@ __global__ __launch_bounds__(BM == 256 ? 512 : 256) void grad_gemm_kernel(
   const int64_t wpr = S.K / 8;
   const int mat_step = (int)(S.Nc / 32);            // first step of matrix 1
 
-  // this thread's chunks of d': row tid / 4 (+ NT / 4), chunk tid % 4
+  // Each step's values are read through buffer descriptors that start at the step's first entry, so
+  // that a thread's offset never changes and entries past the end (rows past M, channels past N)
+  // read as zeros.
+  // This thread's chunks of d': row tid / 4 (+ NT / 4), chunk tid % 4.
   const int ac = tid & 3;
-  const uint16_t *hp[kAT], *lp[kAT];
-  uint32_t awr[kAT];                                // LDS byte offset within P
+  const uint32_t rows = (uint32_t)(S.M - m0 < BM ? S.M - m0 : BM);
+  uint32_t aoff[kAT], awr[kAT];                     // byte offsets: global, within P
 #pragma unroll
   for (int i = 0; i < kAT; ++i) {
     const int row = (tid >> 2) + i * (NT / 4);
-    const int64_t m = m0 + row < S.M ? m0 + row : S.M - 1;
-    hp[i] = hi + m * 32 + ac * 8;
-    lp[i] = LO ? lo + m * 32 + ac * 8 : nullptr;
+    aoff[i] = (uint32_t)(row * 64 + ac * 16);
     awr[i] = (uint32_t)(row * 64 + ((ac ^ ((row >> 2) & 3)) << 4));
   }
   const int64_t grp0 = k0 / G, groups = S.K / G;
   const uint16_t* sp[2];
 #pragma unroll
-  for (int v = 0; v < 2; ++v)
-    sp[v] = st + (grp0 + v < groups ? grp0 + v : groups - 1) * S.C + ac * 8;
+  for (int v = 0; v < 2; ++v) sp[v] = st + (grp0 + v < groups ? grp0 + v : groups - 1) * S.C;
   // this thread's word pairs: channels 2 (t % 16), word t / 16 of the tile
   int bn[kBT];
-  int64_t bw[kBT];
+  uint32_t boff[kBT], bwr[kBT];
   const uint16_t* bsub[kBT];
-  uint32_t bwr[kBT];
-  bool blive[kBT];
 #pragma unroll
   for (int i = 0; i < kBT; ++i) {
-    const int t = tid + i * NT;
-    blive[i] = t < 4 * G;
-    const int w = blive[i] ? t >> 4 : 0;
+    // with fewer pairs than threads the upper threads repeat the lower ones' (a branch would cost more)
+    const int t = (tid + i * NT) % (4 * G);
+    const int w = t >> 4;
     bn[i] = 2 * (t & 15);
-    const int64_t word = k0 / 8 + w;
-    bw[i] = word < wpr ? word : wpr - 1;
-    const int64_t grp = bw[i] / WPG;
-    bsub[i] = ZP ? sub + grp * S.C + bn[i] : nullptr;
+    const int64_t word = k0 / 8 + w < wpr ? k0 / 8 + w : wpr - 1;
+    boff[i] = (uint32_t)((bn[i] * wpr + word) * 4);
+    bsub[i] = ZP ? sub + (word / WPG) * S.C + bn[i] : nullptr;
     // column i8 * WPG + w % WPG of group w / WPG, i8 = 0..7: row offset added at the write
     bwr[i] = (uint32_t)((w / WPG) * G + w % WPG);
   }
-  struct Regs {
-    uint4 h[kAT], l[kAT], s[2];
-    uint32_t q[kBT][2], z[kBT];
+  // one step's values in flight
+  uint4 rh[kAT], rl[kAT], rs[2];
+  uint32_t rq[kBT][2], rz[kBT];
+  auto entries = [&](const uint16_t* p, int t) {    // step t of hi or lo, from row m0 on
+    return make_rsrc(p + ((int64_t)t * S.M + m0) * 32, rows * 64u);
   };
-  auto load = [&](int t, Regs& R) {
-    const int64_t off = (int64_t)t * S.M * 32;
-#pragma unroll
-    for (int i = 0; i < kAT; ++i) {
-      R.h[i] = *reinterpret_cast<const uint4*>(hp[i] + off);
-      if (LO) R.l[i] = *reinterpret_cast<const uint4*>(lp[i] + off);
-    }
-#pragma unroll
-    for (int v = 0; v < 2; ++v) R.s[v] = *reinterpret_cast<const uint4*>(sp[v] + (int64_t)t * 32);
+  auto codes = [&](int t) {                          // step t's rows of its matrix
     const int mat = t >= mat_step ? 1 : 0;
-    const int64_t nb = (int64_t)(t - mat * mat_step) * 32;
-    const uint32_t* q = W.q[mat];
-#pragma unroll
-    for (int i = 0; i < kBT; ++i) {
-      if (4 * G < NT && !blive[i]) continue;
-      const int64_t n = nb + bn[i];
-      R.q[i][0] = q[(n < S.N ? n : S.N - 1) * wpr + bw[i]];
-      R.q[i][1] = q[(n + 1 < S.N ? n + 1 : S.N - 1) * wpr + bw[i]];
-      if (ZP) R.z[i] = *reinterpret_cast<const uint32_t*>(bsub[i] + (int64_t)t * 32);
-    }
+    const int64_t n = (int64_t)(t - mat * mat_step) * 32;
+    const int64_t left = S.N - n < 32 ? S.N - n : 32;
+    return make_rsrc(W.q[mat] + n * wpr, (uint32_t)(left * wpr * 4));
   };
-  auto put = [&](int stage, const Regs& R) {
-    char* base = smem + stage * kStage;
+  auto load_a = [&](int t, int i) {
+    rh[i] = buffer_load16(entries(hi, t), aoff[i]);
+    if (LO) rl[i] = buffer_load16(entries(lo, t), aoff[i]);
+  };
+  auto load_s = [&](int t) {
 #pragma unroll
-    for (int i = 0; i < kAT; ++i) {
-      const uint32_t h[4] = {R.h[i].x, R.h[i].y, R.h[i].z, R.h[i].w};
-      const uint32_t l[4] = {LO ? R.l[i].x : 0u, LO ? R.l[i].y : 0u, LO ? R.l[i].z : 0u,
-                             LO ? R.l[i].w : 0u};
+    for (int v = 0; v < 2; ++v) rs[v] = buffer_load16(make_rsrc(sp[v] + (int64_t)t * 32, 64u), ac * 16u);
+  };
+  auto load_b = [&](int t, int i) {
+    const rsrc_t r = codes(t);
+    rq[i][0] = buffer_load4(r, boff[i]);
+    rq[i][1] = buffer_load4(r, boff[i] + (uint32_t)(wpr * 4));
+    if (ZP) rz[i] = *reinterpret_cast<const uint32_t*>(bsub[i] + (int64_t)t * 32);
+  };
+  // chunk i of d' folded with column group v's steps, into P
+  auto fold = [&](char* base, int i, int v) {
+    const uint32_t h[4] = {rh[i].x, rh[i].y, rh[i].z, rh[i].w};
+    const uint32_t l[4] = {LO ? rl[i].x : 0u, LO ? rl[i].y : 0u, LO ? rl[i].z : 0u, LO ? rl[i].w : 0u};
+    const uint32_t s[4] = {rs[v].x, rs[v].y, rs[v].z, rs[v].w};
+    uint32_t p[4];
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const uint32_t s[4] = {R.s[v].x, R.s[v].y, R.s[v].z, R.s[v].w};
-        uint32_t p[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const half2_t hv = __builtin_bit_cast(half2_t, h[j]);
-          const half2_t sv = __builtin_bit_cast(half2_t, s[j]);
-          half2_t pv;
-          if constexpr (LO)
-            pv = __builtin_elementwise_fma(hv, sv, __builtin_bit_cast(half2_t, l[j]) * sv);
-          else
-            pv = hv * sv;
-          p[j] = __builtin_bit_cast(uint32_t, pv);
-        }
-        *reinterpret_cast<uint4*>(base + v * kP + awr[i]) = make_uint4(p[0], p[1], p[2], p[3]);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const half2_t hv = __builtin_bit_cast(half2_t, h[j]);
+      const half2_t sv = __builtin_bit_cast(half2_t, s[j]);
+      half2_t pv;
+      if constexpr (LO)
+        pv = __builtin_elementwise_fma(hv, sv, __builtin_bit_cast(half2_t, l[j]) * sv);
+      else
+        pv = hv * sv;
+      p[j] = __builtin_bit_cast(uint32_t, pv);
     }
+    *reinterpret_cast<uint4*>(base + v * kP + awr[i]) = make_uint4(p[0], p[1], p[2], p[3]);
+  };
+  // byte j (columns 2j, 2j + 1) of word pair i
+  auto decode = [&](char* base, int i, int j) {
     constexpr uint32_t kLo = ZP ? 0x64006400u : 0x64086408u;   // exponent, and the flip of bit 3
     constexpr uint32_t kHi = ZP ? 0x64006400u : 0x64806480u;
     const half2_t sixteenth = half2_t{(_Float16)0.0625f, (_Float16)0.0625f};
-#pragma unroll
-    for (int i = 0; i < kBT; ++i) {
-      if (4 * G < NT && !blive[i]) continue;
-      // subtrahends: -(1024 + zc) for the low nibbles, -(64 + zc) for the high ones
-      const half2_t nlo = ZP ? __builtin_bit_cast(half2_t, R.z[i])
-                             : half2_t{(_Float16)-1032.0f, (_Float16)-1032.0f};
-      const half2_t nhi = nlo + half2_t{(_Float16)960.0f, (_Float16)960.0f};
-      const int chunk = bn[i] >> 3, within = (bn[i] & 7) * 2;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t x = __builtin_amdgcn_perm(
-            R.q[i][1], R.q[i][0], 0x0C040C00u + (uint32_t)j * 0x00010001u);
-        const half2_t a = __builtin_bit_cast(half2_t, (x & 0x000F000Fu) ^ kLo) + nlo;
-        const half2_t b = __builtin_elementwise_fma(
-            __builtin_bit_cast(half2_t, (x & 0x00F000F0u) ^ kHi), sixteenth, nhi);
-        const uint32_t ra = bwr[i] + (uint32_t)(2 * j * WPG), rb = ra + WPG;
-        char* d = base + 2 * kP;
-        *reinterpret_cast<uint32_t*>(d + ra * 64 + ((chunk ^ ((ra >> 2) & 3)) << 4) + within) =
-            __builtin_bit_cast(uint32_t, a);
-        *reinterpret_cast<uint32_t*>(d + rb * 64 + ((chunk ^ ((rb >> 2) & 3)) << 4) + within) =
-            __builtin_bit_cast(uint32_t, b);
-      }
+    // subtrahends: -(1024 + zc) for the low nibbles, -(64 + zc) for the high ones
+    const half2_t nlo = ZP ? __builtin_bit_cast(half2_t, rz[i])
+                           : half2_t{(_Float16)-1032.0f, (_Float16)-1032.0f};
+    const half2_t nhi = nlo + half2_t{(_Float16)960.0f, (_Float16)960.0f};
+    const uint32_t x = __builtin_amdgcn_perm(rq[i][1], rq[i][0],
+                                             0x0C040C00u + (uint32_t)j * 0x00010001u);
+    const half2_t a = __builtin_bit_cast(half2_t, (x & 0x000F000Fu) ^ kLo) + nlo;
+    const half2_t b = __builtin_elementwise_fma(
+        __builtin_bit_cast(half2_t, (x & 0x00F000F0u) ^ kHi), sixteenth, nhi);
+    const int chunk = bn[i] >> 3, within = (bn[i] & 7) * 2;
+    const uint32_t ra = bwr[i] + (uint32_t)(2 * j * WPG), rb = ra + WPG;
+    char* d = base + 2 * kP + within;
+    *reinterpret_cast<uint32_t*>(d + ra * 64 + ((chunk ^ ((ra >> 2) & 3)) << 4)) =
+        __builtin_bit_cast(uint32_t, a);
+    *reinterpret_cast<uint32_t*>(d + rb * 64 + ((chunk ^ ((rb >> 2) & 3)) << 4)) =
+        __builtin_bit_cast(uint32_t, b);
+  };
+  // the staging of a step in pieces: folds of the chunks, then bytes of the word pairs; each set of
+  // registers is loaded again, for step `t`, as soon as its last piece is done
+  constexpr int kPieces = 2 * kAT + 4 * kBT;
+  auto piece = [&](char* base, int x, int t) {
+    if (x < 2 * kAT) {
+      fold(base, x >> 1, x & 1);
+      if (x & 1) load_a(t, x >> 1);
+      if (x == 2 * kAT - 1) load_s(t);
+    } else if (x < kPieces) {
+      const int y = x - 2 * kAT;
+      decode(base, y >> 2, y & 3);
+      if ((y & 3) == 3) load_b(t, y >> 2);
     }
   };
 
@@ -373,50 +374,55 @@ __global__ __launch_bounds__(BM == 256 ? 512 : 256) void grad_gemm_kernel(
 #pragma unroll
   for (int h = 0; h < 2; ++h)
     foff[h] = (uint32_t)(l32 * 64 + (((2 * h + lh) ^ ((l32 >> 2) & 3)) << 4));
-  auto compute = [&](int stage) {
-    const char* pa = smem + stage * kStage + vg * kP + mq * RM * 64;
-    const char* pb = smem + stage * kStage + 2 * kP + vg * G * 64;
+  // Step t computes from stage `cur` while step t + 1's values go into the other stage and step
+  // t + 2's are loaded. The pieces stand between the matrix instructions, which run in their shadow
+  // (left to the compiler, they all came first: TIMES). Nothing here is conditional (the last step
+  // loads the slice's last step again and writes a stage nobody reads): behind a branch the compiler
+  // has to wait for the newest loads before it uses the older ones.
+  constexpr int kM = 2 * MBLK * NBLK, kPer = (kPieces + kM - 1) / kM;
+  const int last = s1 - 1;
+  auto step = [&](int t, int cur) {
+    __syncthreads();                                 // `cur` is written, the other stage read
+    const char* pa = smem + cur * kStage + vg * kP + mq * RM * 64;
+    const char* pb = smem + cur * kStage + 2 * kP + vg * G * 64;
+    char* other = smem + (cur ^ 1) * kStage;
+    const int tl = t + 2 < last ? t + 2 : last;
+    half8_t a[2][MBLK], b[2][NBLK];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      half8_t a[MBLK], b[NBLK];
+    for (int i = 0; i < MBLK; ++i)
+      a[0][i] = *reinterpret_cast<const half8_t*>(pa + i * 32 * 64 + foff[0]);
 #pragma unroll
-      for (int i = 0; i < MBLK; ++i)
-        a[i] = *reinterpret_cast<const half8_t*>(pa + i * 32 * 64 + foff[h]);
+    for (int j = 0; j < NBLK; ++j)
+      b[0][j] = *reinterpret_cast<const half8_t*>(pb + j * 32 * 64 + foff[0]);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < NBLK; ++j)
-        b[j] = *reinterpret_cast<const half8_t*>(pb + j * 32 * 64 + foff[h]);
+    for (int x = 0; x < kM; ++x) {
+      const int h = x / (MBLK * NBLK), y = x % (MBLK * NBLK), j = y / MBLK, i = y % MBLK;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[h][i], b[h][j], acc[i][j], 0, 0, 0);
+      // fragments of the second half
+      if (x < MBLK) a[1][x] = *reinterpret_cast<const half8_t*>(pa + x * 32 * 64 + foff[1]);
+      if (x < NBLK) b[1][x] = *reinterpret_cast<const half8_t*>(pb + x * 32 * 64 + foff[1]);
 #pragma unroll
-      for (int i = 0; i < MBLK; ++i)
-#pragma unroll
-        for (int j = 0; j < NBLK; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[i], b[j], acc[i][j], 0, 0, 0);
+      for (int k = 0; k < kPer; ++k) piece(other, x * kPer + k, tl);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
-  // The loads and the writes are unconditional (the last steps load the slice's last step again and
-  // write a stage nobody reads): behind a branch the compiler has to wait for the newest loads
-  // before it uses the older ones (1285 us instead of LOOPTIME for 4096 rows of 2 x 11008 x 4096).
-  const int last = s1 - 1;
-  Regs R[2];
-  load(s0, R[0]);
-  load(s0 < last ? s0 + 1 : last, R[1]);
-  put(0, R[0]);
-  // step t (stage t & 1 from s0): registers of step t + 1 are in nxt, cur's are free
-  auto step = [&](int t, int stage, Regs& cur, Regs& nxt) {
-    __syncthreads();                                 // stage written, other stage read
-    load(t + 2 < last ? t + 2 : last, cur);
-    put(stage ^ 1, nxt);
-    compute(stage);
-  };
+  // prologue: step s0 staged, step s0 + 1 in the registers
+  const int second = s0 < last ? s0 + 1 : last;
+#pragma unroll
+  for (int i = 0; i < kAT; ++i) load_a(s0, i);
+  load_s(s0);
+#pragma unroll
+  for (int i = 0; i < kBT; ++i) load_b(s0, i);
+#pragma unroll
+  for (int x = 0; x < kPieces; ++x) piece(smem, x, second);
   int t = s0;
   for (; t + 1 < s1; t += 2) {
-    step(t, 0, R[0], R[1]);
-    step(t + 1, 1, R[1], R[0]);
+    step(t, 0);
+    step(t + 1, 1);
   }
-  if (t < s1) {
-    __syncthreads();
-    compute(0);
-  }
+  if (t < s1) step(t, 0);
 
   // ---- store: a lane's block j holds column 8 w + i8, w = lane % WPG -------------------------
   const int64_t kl = k0 + vg * G + 8 * (l32 % WPG) + l32 / WPG;   // of block 0; + 32 / WPG per block
