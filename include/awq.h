@@ -429,8 +429,8 @@ awq_status awq_act_stats_noalloc(const void* X, awq_dtype xdt, int64_t M, int64_
  *          which the block's largest finite |x| is at most 448 2^e; 1 for a block without a
  *          non-zero finite value. A power of two: x / scale is exact, and code * scale is exact
  *          in bf16 and fp32.
- * flags    in/out: NONFINITE_X (an Inf or NaN, whose code is NaN; the block's scale is that of its
- *          finite values).
+ * flags    in/out, or NULL: NONFINITE_X (an Inf or NaN, whose code is NaN; the block's scale is
+ *          that of its finite values).
  * Errors: AWQ_ERR_NULL, AWQ_ERR_DTYPE, AWQ_ERR_CONFIG (block_rows), AWQ_ERR_SHAPE (sizes, ldx,
  *         misalignment; more than 2^31 blocks of one row).
  * ---------------------------------------------------------------------------------------- */
@@ -500,7 +500,7 @@ awq_status w4a16_gated(const uint16_t* A, int64_t M, int64_t N, int64_t K, int32
  * awq_fp8_quantize's format with block_rows 1, cut from the fp32 sums.
  * g8, u8   out, uint8 [M, N], 16-byte aligned, N % 16 == 0; g_scales, u_scales out, fp32
  *          [M, ceil(N/128)].
- * flags    in/out: NONFINITE_ACT (the value's code is NaN).
+ * flags    in/out, or NULL: NONFINITE_ACT (the value's code is NaN).
  * ws       as w4a16_gated, of w4a16_gated_workspace_bytes(M, N, K, 1) bytes.
  * Errors: as w4a16_gated; AWQ_ERR_SHAPE also when N % 16 != 0.
  * ---------------------------------------------------------------------------------------- */

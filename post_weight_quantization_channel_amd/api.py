@@ -451,13 +451,37 @@ FP8 = torch.float8_e4m3fn
 class Fp8Result:
     q: torch.Tensor        # float8_e4m3fn [M, K]
     scales: torch.Tensor   # fp32 [ceil(M / block_rows), ceil(K / 128)], powers of two
-    flags: torch.Tensor
+    flags: torch.Tensor | None = None   # the tensor given to the call
 
 
 def _same_device(ref: torch.Tensor, *named) -> None:
     for t, nm in named:
         if t is not None and t.device != ref.device:
             raise ValueError(f"{nm} must be on {ref.device}")
+
+
+def _flags_arg(flags, device):
+    """The pointer of an optional flag word."""
+    if flags is None:
+        return None
+    _dev(flags, "flags")
+    if flags.dtype != torch.int32 or flags.numel() != 1 or flags.device != device:
+        raise ValueError(f"flags must be int32 [1] on {device}")
+    return flags.data_ptr()
+
+
+def _launch(call: str, fn, device: torch.device, *args) -> None:
+    """fn(*args, stream) on the current stream of `device`, with that device current. (The raw
+    stream handle and the check before the device guard keep a small call's host time near the
+    launch itself.)"""
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status:
+        check(call, status)
 
 
 def _out(out, shape, dtype, device) -> torch.Tensor:
@@ -498,7 +522,8 @@ def fp8_quantize(X: torch.Tensor, block_rows: int = 1,
                  flags: torch.Tensor | None = None) -> Fp8Result:
     """X in 8 bits: e4m3 codes with one power-of-two scale per block of 128 columns by 1 row
     (activations) or 128 rows (weights). X may be a row-strided view (unit column stride, row
-    stride a multiple of 8 elements); its columns are a multiple of 16."""
+    stride a multiple of 8 elements); its columns are a multiple of 16. flags: an int32 [1] tensor
+    that collects the library's flag bits, or None for none."""
     lib = _lib.load()
     if not X.is_cuda or X.dim() != 2 or (X.stride(1) != 1 and X.shape[1] > 1):
         raise ValueError("X must be a 2-D device tensor with unit column stride")
@@ -508,14 +533,12 @@ def fp8_quantize(X: torch.Tensor, block_rows: int = 1,
         raise ValueError("block_rows must be 1 or 128")
     M, K = X.shape
     dev = X.device
-    flags = _flags(dev, flags)
-    _same_device(X, (flags, "flags"))
+    fl = _flags_arg(flags, dev)
     q = torch.empty((M, K), dtype=FP8, device=dev)
     scales = torch.empty(_blocks_shape(M, K, block_rows), dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        check("awq_fp8_quantize", lib.awq_fp8_quantize(
-            X.data_ptr(), _DT[X.dtype], M, K, X.stride(0) if M > 1 else K, block_rows,
-            q.data_ptr(), scales.data_ptr(), flags.data_ptr(), _stream(X)))
+    _launch("awq_fp8_quantize", lib.awq_fp8_quantize, dev,
+        X.data_ptr(), _DT[X.dtype], M, K, X.stride(0) if M > 1 else K, block_rows,
+        q.data_ptr(), scales.data_ptr(), fl)
     return Fp8Result(q, scales, flags)
 
 
@@ -532,10 +555,8 @@ def fp8_dequantize(q: torch.Tensor, scales: torch.Tensor, block_rows: int = 1,
     _same_device(q, (scales, "scales"))
     M, K = q.shape
     out = _out(out, (M, K), dtype, q.device)
-    with torch.cuda.device(q.device):
-        check("awq_fp8_dequantize", lib.awq_fp8_dequantize(
-            q.data_ptr(), scales.data_ptr(), M, K, block_rows, _DT[dtype], out.data_ptr(),
-            _stream(q)))
+    _launch("awq_fp8_dequantize", lib.awq_fp8_dequantize, q.device,
+        q.data_ptr(), scales.data_ptr(), M, K, block_rows, _DT[dtype], out.data_ptr())
     return out
 
 
@@ -562,11 +583,10 @@ def fp8_gemm(A8: torch.Tensor, a_scales: torch.Tensor, W8: torch.Tensor, w_scale
     _same_device(A8, (a_scales, "a_scales"), (W8, "W8"), (w_scales, "w_scales"))
     out = _out(out, (M, N), out_dtype, dev)
     ws = _scratch(workspace, lib.awq_fp8_gemm_workspace_bytes(M, N, K), dev)
-    with torch.cuda.device(dev):
-        check("awq_fp8_gemm", lib.awq_fp8_gemm(
-            A8.data_ptr(), a_scales.data_ptr(), W8.data_ptr(), w_scales.data_ptr(), M, N, K,
-            _DT[out_dtype], out.data_ptr(), ws.data_ptr() if ws is not None else None,
-            ws.numel() * ws.element_size() if ws is not None else 0, _stream(A8)))
+    _launch("awq_fp8_gemm", lib.awq_fp8_gemm, dev,
+        A8.data_ptr(), a_scales.data_ptr(), W8.data_ptr(), w_scales.data_ptr(), M, N, K,
+        _DT[out_dtype], out.data_ptr(), ws.data_ptr() if ws is not None else None,
+        ws.numel() * ws.element_size() if ws is not None else 0)
     return out
 
 
@@ -639,10 +659,9 @@ def w4a16_gated(A: torch.Tensor, gate_qweight: torch.Tensor, gate_scales16: torc
     N = _gated_check(A, K, gate, up, group, act)
     out = _out(out, (M, N), torch.float16, A.device)
     ws = _scratch(workspace, lib.w4a16_gated_workspace_bytes(M, N, K, 0), A.device)
-    with torch.cuda.device(A.device):
-        check("w4a16_gated", lib.w4a16_gated(
-            A.data_ptr(), M, N, K, group, _ACTS[act], _packed_arg(*gate), _packed_arg(*up),
-            out.data_ptr(), *_ws_args(ws), _stream(A)))
+    _launch("w4a16_gated", lib.w4a16_gated, A.device,
+        A.data_ptr(), M, N, K, group, _ACTS[act], _packed_arg(*gate), _packed_arg(*up),
+        out.data_ptr(), *_ws_args(ws))
     return out
 
 
@@ -653,7 +672,7 @@ class GatedResult:
     g_scales: torch.Tensor   # fp32 [M, ceil(N / 128)]
     u8: torch.Tensor         # float8_e4m3fn [M, N]: A Wu^T
     u_scales: torch.Tensor
-    flags: torch.Tensor
+    flags: torch.Tensor | None = None
 
 
 def w4a16_gated_ckpt(A: torch.Tensor, gate_qweight: torch.Tensor, gate_scales16: torch.Tensor,
@@ -662,7 +681,7 @@ def w4a16_gated_ckpt(A: torch.Tensor, gate_qweight: torch.Tensor, gate_scales16:
                      up_zeros: torch.Tensor | None = None, flags: torch.Tensor | None = None,
                      workspace: torch.Tensor | None = None) -> GatedResult:
     """w4a16_gated that also keeps both projections in 8 bits (fp8_quantize's format, blocks of
-    1 x 128) for w4a16_gated_backward; N a multiple of 16."""
+    1 x 128) for w4a16_gated_backward; N a multiple of 16. flags as in fp8_quantize."""
     lib = _lib.load()
     _halves(A, "A")
     M, K = A.shape
@@ -670,18 +689,17 @@ def w4a16_gated_ckpt(A: torch.Tensor, gate_qweight: torch.Tensor, gate_scales16:
     up = (up_qweight, up_scales16, up_zeros)
     N = _gated_check(A, K, gate, up, group, act)
     dev = A.device
-    flags = _flags(dev, flags)
-    _same_device(A, (flags, "flags"))
+    fl = _flags_arg(flags, dev)
     H = torch.empty((M, N), dtype=torch.float16, device=dev)
-    q = torch.empty((2, M, N), dtype=FP8, device=dev)
-    s = torch.empty((2, *_blocks_shape(M, N, 1)), dtype=torch.float32, device=dev)
+    g8, u8 = (torch.empty((M, N), dtype=FP8, device=dev) for _ in range(2))
+    gs, us = (torch.empty(_blocks_shape(M, N, 1), dtype=torch.float32, device=dev)
+              for _ in range(2))
     ws = _scratch(workspace, lib.w4a16_gated_workspace_bytes(M, N, K, 1), dev)
-    with torch.cuda.device(dev):
-        check("w4a16_gated_ckpt", lib.w4a16_gated_ckpt(
-            A.data_ptr(), M, N, K, group, _ACTS[act], _packed_arg(*gate), _packed_arg(*up),
-            H.data_ptr(), q[0].data_ptr(), s[0].data_ptr(), q[1].data_ptr(), s[1].data_ptr(),
-            flags.data_ptr(), *_ws_args(ws), _stream(A)))
-    return GatedResult(H, q[0], s[0], q[1], s[1], flags)
+    _launch("w4a16_gated_ckpt", lib.w4a16_gated_ckpt, dev,
+        A.data_ptr(), M, N, K, group, _ACTS[act], _packed_arg(*gate), _packed_arg(*up),
+        H.data_ptr(), g8.data_ptr(), gs.data_ptr(), u8.data_ptr(), us.data_ptr(),
+        fl, *_ws_args(ws))
+    return GatedResult(H, g8, gs, u8, us, flags)
 
 
 def w4a16_gated_backward_workspace_bytes(M: int, N: int, K: int, group: int = 128,
@@ -714,11 +732,10 @@ def w4a16_gated_backward(dH: torch.Tensor, g8: torch.Tensor, g_scales: torch.Ten
     out = _out(out, (M, K), torch.float16, dH.device)
     ws = _scratch(workspace, lib.w4a16_gated_backward_workspace_bytes(
         M, N, K, group, int(gate_zeros is not None)), dH.device)
-    with torch.cuda.device(dH.device):
-        check("w4a16_gated_backward", lib.w4a16_gated_backward(
-            dH.data_ptr(), g8.data_ptr(), g_scales.data_ptr(), u8.data_ptr(), u_scales.data_ptr(),
-            M, N, K, group, _ACTS[act], _packed_arg(*gate), _packed_arg(*up), out.data_ptr(),
-            *_ws_args(ws), _stream(dH)))
+    _launch("w4a16_gated_backward", lib.w4a16_gated_backward, dH.device,
+        dH.data_ptr(), g8.data_ptr(), g_scales.data_ptr(), u8.data_ptr(), u_scales.data_ptr(),
+        M, N, K, group, _ACTS[act], _packed_arg(*gate), _packed_arg(*up), out.data_ptr(),
+        *_ws_args(ws))
     return out
 
 
@@ -747,10 +764,8 @@ def w4a16_gemm_backward(dY: torch.Tensor, qweight: torch.Tensor, scales16: torch
     out = _out(out, (M, K), torch.float16, dY.device)
     ws = _scratch(workspace, lib.w4a16_gemm_backward_workspace_bytes(
         M, N, K, group, int(zeros is not None)), dY.device)
-    with torch.cuda.device(dY.device):
-        check("w4a16_gemm_backward", lib.w4a16_gemm_backward(
-            dY.data_ptr(), M, N, K, group, qweight.data_ptr(), scales16.data_ptr(),
-            zeros.data_ptr() if zeros is not None else None,
-            s16.data_ptr() if s16 is not None else None, out.data_ptr(), *_ws_args(ws),
-            _stream(dY)))
+    _launch("w4a16_gemm_backward", lib.w4a16_gemm_backward, dY.device,
+        dY.data_ptr(), M, N, K, group, qweight.data_ptr(), scales16.data_ptr(),
+        zeros.data_ptr() if zeros is not None else None,
+        s16.data_ptr() if s16 is not None else None, out.data_ptr(), *_ws_args(ws))
     return out

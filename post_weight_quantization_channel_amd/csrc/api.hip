@@ -601,7 +601,7 @@ awq_status check_fp8_gemm(int64_t M, int64_t N, int64_t K) {
 awq_status awq_fp8_quantize(const void* X, awq_dtype xdt, int64_t M, int64_t K, int64_t ldx,
                             int32_t block_rows, uint8_t* q, float* scales, uint32_t* flags,
                             hipStream_t stream) {
-  if (!X || !q || !scales || !flags) return AWQ_ERR_NULL;
+  if (!X || !q || !scales) return AWQ_ERR_NULL;   // flags NULL: not reported
   if (!valid_dtype(xdt)) return AWQ_ERR_DTYPE;
   if (block_rows != 1 && block_rows != 128) return AWQ_ERR_CONFIG;
   if (!fp8_matrix_ok(M, K, block_rows) || ldx < K || ldx % 8 || ldx > kMaxDim || !aligned16(X) ||
@@ -704,7 +704,7 @@ awq_status w4a16_gated_ckpt(const uint16_t* A, int64_t M, int64_t N, int64_t K, 
                             int32_t act, const awq_packed* gate, const awq_packed* up, uint16_t* H,
                             uint8_t* g8, float* g_scales, uint8_t* u8, float* u_scales,
                             uint32_t* flags, void* ws, size_t ws_bytes, hipStream_t stream) {
-  if (!A || !H || !g8 || !g_scales || !u8 || !u_scales || !flags) return AWQ_ERR_NULL;
+  if (!A || !H || !g8 || !g_scales || !u8 || !u_scales) return AWQ_ERR_NULL;
   const awq_status cs = check_gated(M, N, K, group, act, gate, up);
   if (cs != AWQ_OK) return cs;
   if (!saved_sizes_ok(N) || !aligned16(A) || !aligned16(H) || !aligned16(g8) || !aligned16(u8) ||

@@ -43,7 +43,7 @@ __global__ __launch_bounds__(256) void fp8_quantize_rows_kernel(
     *reinterpret_cast<uint2*>(q + (int64_t)row * K + k) = fp8_pack8(v, s.inv, bad);
   }
   if (in && l == 0) scales[b] = s.scale;
-  wave_flag(flags, bad != 0u, kFlagNonfiniteX);
+  if (flags) wave_flag(flags, bad != 0u, kFlagNonfiniteX);
 }
 
 // One 128 x 128 block per workgroup of 256 threads; blockIdx.x = row block * KB + column block.
@@ -81,7 +81,7 @@ __global__ __launch_bounds__(256) void fp8_quantize_tiles_kernel(
     }
   }
   if (threadIdx.x == 0) scales[blockIdx.x] = s.scale;
-  wave_flag(flags, any != 0u, kFlagNonfiniteX);
+  if (flags) wave_flag(flags, any != 0u, kFlagNonfiniteX);
 }
 
 // 16 codes per thread (K % 16 == 0, so they lie in one row and one block). units = M K / 16.

@@ -566,7 +566,7 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
             cl[r * TM * 128 + row * 128 + 32 * wave + 16 * h + li] = (char)code;
           }
         }
-    wave_flag(O.flags, any, kFlagNonfiniteAct);
+    if (O.flags) wave_flag(O.flags, any, kFlagNonfiniteAct);
   }
   __syncthreads();
   for (int e = tid; e < TM * 16; e += 256) {   // 16 bytes of H each
@@ -649,7 +649,7 @@ __global__ __launch_bounds__(256) void w4a16_gated_finish_kernel(
             fp8_pack8(v[r], s.inv, bad);
       if (in && (threadIdx.x & 15) == 0) (r == 0 ? O.gs : O.us)[b] = s.scale;
     }
-    wave_flag(O.flags, in && any != 0u, kFlagNonfiniteAct);
+    if (O.flags) wave_flag(O.flags, in && any != 0u, kFlagNonfiniteAct);
   }
 }
 

@@ -58,33 +58,49 @@ __device__ __forceinline__ void grad_step_maxima(const GatedWeights& W, const Gr
   for (int g = threadIdx.x; g < groups; g += blockDim.x) pmax[part * groups + g] = lds[g];
 }
 
-// One workgroup: 32 channels of the contraction, all groups of columns. st [groups][C] fp16 step',
-// sub [groups][C] fp16 -(1024 + z) (ZP), colscale [groups] fp32 2^f.
+// One workgroup: 32 channels of the contraction, up to 128 groups of columns at a time (read along
+// the rows, written along the channels, through LDS). st [groups][C] fp16 step', sub [groups][C]
+// fp16 -(1024 + z) (ZP), colscale [groups] fp32 2^f.
 template <bool ZP>
 __global__ __launch_bounds__(256) void grad_steps_kernel(GatedWeights W, GradShape S, int groups,
                                                          const uint32_t* __restrict__ pmax,
                                                          uint16_t* __restrict__ st,
                                                          uint16_t* __restrict__ sub,
                                                          float* __restrict__ colscale) {
-  __shared__ uint32_t expo[kMaxGroups];   // biased exponent of 2^f
-  for (int g = threadIdx.x; g < groups; g += 256) {
-    uint32_t u = 0u;
-#pragma unroll 8
-    for (int p = 0; p < kParts; ++p) u = max(u, pmax[p * groups + g]);
-    // the power of two at or above the largest step; 1 for 0 and for a non-finite step
-    expo[g] = (u == 0u || u >= 0x7F800000u) ? 127u : (u + 0x7FFFFFu) >> 23;
-    if (blockIdx.x == 0) colscale[g] = __uint_as_float(expo[g] << 23);
-  }
-  __syncthreads();
+  constexpr int kTG = 128;
+  __shared__ uint32_t expo[kTG];   // biased exponent of 2^f
+  __shared__ uint16_t tile[32 * kTG];
+  __shared__ uint8_t ztile[ZP ? 32 * kTG : 1];
   const int64_t c0 = (int64_t)blockIdx.x * 32;
   const int mat = c0 >= S.Nc ? 1 : 0;
-  const int64_t n = c0 - mat * S.Nc + (threadIdx.x & 31);
-  const bool ok = n < S.N;
-  for (int g = threadIdx.x >> 5; g < groups; g += 8) {
-    const int64_t at = (int64_t)g * S.C + c0 + (threadIdx.x & 31);
-    const float inv = __uint_as_float((254u - expo[g]) << 23);
-    st[at] = ok ? f2h(h2f(W.s[mat][n * groups + g]) * inv) : (uint16_t)0;
-    if (ZP) sub[at] = f2h(-1024.0f - (ok ? (float)W.z[mat][n * groups + g] : 0.0f));
+  const int64_t n0 = c0 - mat * S.Nc;
+  const int rows = (int)(S.N - n0 < 32 ? S.N - n0 : 32);
+  for (int g0 = 0; g0 < groups; g0 += kTG) {
+    const int ng = groups - g0 < kTG ? groups - g0 : kTG;
+    if (g0) __syncthreads();
+    for (int e = threadIdx.x; e < rows * ng; e += 256) {
+      const int r = e / ng, g = e - r * ng;
+      const int64_t at = (n0 + r) * groups + g0 + g;
+      tile[r * kTG + g] = W.s[mat][at];
+      if (ZP) ztile[r * kTG + g] = W.z[mat][at];
+    }
+    if ((int)threadIdx.x < ng) {
+      const int g = threadIdx.x;
+      uint32_t u = 0u;
+#pragma unroll 16
+      for (int p = 0; p < kParts; ++p) u = max(u, pmax[p * groups + g0 + g]);
+      // the power of two at or above the largest step; 1 for 0 and for a non-finite step
+      expo[g] = (u == 0u || u >= 0x7F800000u) ? 127u : (u + 0x7FFFFFu) >> 23;
+      if (blockIdx.x == 0) colscale[g0 + g] = __uint_as_float(expo[g] << 23);
+    }
+    __syncthreads();
+    const int r = threadIdx.x & 31;
+    for (int g = threadIdx.x >> 5; g < ng; g += 8) {
+      const int64_t at = (int64_t)(g0 + g) * S.C + c0 + r;
+      const float inv = __uint_as_float((254u - expo[g]) << 23);
+      st[at] = r < rows ? f2h(h2f(tile[r * kTG + g]) * inv) : (uint16_t)0;
+      if (ZP) sub[at] = f2h(-1024.0f - (r < rows ? (float)ztile[r * kTG + g] : 0.0f));
+    }
   }
 }
 
@@ -104,26 +120,26 @@ __device__ __forceinline__ void load8_halves(const uint16_t* p, int64_t n, int64
   }
 }
 
-// WPR waves per row (1: four rows per workgroup of 4 waves; 8: one row). Pass 1 finds the row's
-// largest |d|, pass 2 forms the values again, scales and stores them. The last kParts workgroups
-// find the largest steps instead.
-template <bool GATED, int ACT, int WPR>
-__global__ __launch_bounds__(WPR == 1 ? 256 : 512) void grad_rows_kernel(
+// One workgroup of 512 threads per row, which first finds the row's largest |d|. IT > 0: the row is at
+// most IT x 4096 channels and stays in registers meanwhile; IT = 0: any length, the values are
+// formed twice (gated, 4096 rows of 11008: 190 us that way, 134 in registers). Consecutive rows go
+// to one XCD, whose L2 then joins their 64-byte pieces of a line. The last kParts workgroups find
+// the largest steps instead.
+template <bool GATED, int ACT, int IT>
+__global__ __launch_bounds__(512) void grad_rows_kernel(
     const uint16_t* __restrict__ dY, GatedSaved V, GatedWeights W, GradShape S, int groups,
     uint16_t* __restrict__ hi, uint16_t* __restrict__ lo, float* __restrict__ unscale,
     uint32_t* __restrict__ pmax) {
   __shared__ uint32_t wmax[8];
   __shared__ uint32_t gmax[kMaxGroups];
-  if (blockIdx.x >= gridDim.x - kParts) {
-    grad_step_maxima(W, S, GATED ? 2 : 1, groups, (int)(blockIdx.x - (gridDim.x - kParts)), pmax,
-                     gmax);
+  const uint32_t M = (uint32_t)S.M;
+  if (blockIdx.x >= M) {
+    grad_step_maxima(W, S, GATED ? 2 : 1, groups, (int)(blockIdx.x - M), pmax, gmax);
     return;
   }
+  const uint32_t xcd = blockIdx.x & 7u, rem = M & 7u;
+  const int64_t m = xcd * (M >> 3) + (xcd < rem ? xcd : rem) + (blockIdx.x >> 3);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t m = WPR == 1 ? (int64_t)blockIdx.x * 4 + wave : blockIdx.x;
-  if (WPR == 1 && m >= S.M) return;
-  const int t0 = WPR == 1 ? lane : (int)threadIdx.x;
-  constexpr int kStride = 64 * WPR * 8;
   const int64_t KB = (S.N + 127) / 128;
   const uint16_t* row = dY + m * S.N;
 
@@ -163,32 +179,43 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 512) void grad_rows_kernel(
   };
 
   uint32_t mx = 0u;
-  for (int64_t n = 8 * (int64_t)t0; n < S.Nc; n += kStride) {
-    float d0[8], d1[8];
-    values(n, d0, d1);
+  auto largest = [&](const float (&d)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      mx = max(mx, __float_as_uint(d0[i]) & 0x7FFFFFFFu);
-      if (GATED) mx = max(mx, __float_as_uint(d1[i]) & 0x7FFFFFFFu);
+    for (int i = 0; i < 8; ++i) mx = max(mx, __float_as_uint(d[i]) & 0x7FFFFFFFu);
+  };
+  const int64_t first = 8 * (int64_t)threadIdx.x;
+  constexpr int kIt = IT > 0 ? IT : 1, kMat = GATED ? 2 : 1;
+  float d[kMat][kIt][8];
+  if constexpr (IT > 0) {
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      if (first + 4096 * it >= S.Nc) continue;
+      values(first + 4096 * it, d[0][it], d[kMat - 1][it]);
+      largest(d[0][it]);
+      if (GATED) largest(d[kMat - 1][it]);
+    }
+  } else {
+    for (int64_t n = first; n < S.Nc; n += 4096) {
+      values(n, d[0][0], d[kMat - 1][0]);
+      largest(d[0][0]);
+      if (GATED) largest(d[kMat - 1][0]);
     }
   }
 #pragma unroll
   for (int k = 32; k >= 1; k >>= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, k));
-  if constexpr (WPR > 1) {
-    if (lane == 0) wmax[wave] = mx;
-    __syncthreads();
+  if (lane == 0) wmax[wave] = mx;
+  __syncthreads();
 #pragma unroll
-    for (int w = 0; w < WPR; ++w) mx = max(mx, wmax[w]);
-  }
+  for (int w = 0; w < 8; ++w) mx = max(mx, wmax[w]);
   const int e = escale_for_max(__uint_as_float(mx));   // 0 for 0 and for Inf or NaN
   const float sc = ldexpf(1.0f, e);
-  if ((WPR == 1 ? lane : (int)threadIdx.x) == 0) unscale[m] = ldexpf(1.0f, -e);
+  if (threadIdx.x == 0) unscale[m] = ldexpf(1.0f, -e);
 
-  auto put = [&](int64_t c, const float (&d)[8]) {
+  auto put = [&](int64_t c, const float (&v)[8]) {
     uint32_t h[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float a = d[2 * i] * sc, b = d[2 * i + 1] * sc;
+      const float a = v[2 * i] * sc, b = v[2 * i + 1] * sc;
       h[i] = f2h2(a, b);
       if (GATED) {
         const float ha = h2f((uint16_t)(h[i] & 0xFFFFu)), hb = h2f((uint16_t)(h[i] >> 16));
@@ -200,11 +227,20 @@ __global__ __launch_bounds__(WPR == 1 ? 256 : 512) void grad_rows_kernel(
     *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
     if (GATED) *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
   };
-  for (int64_t n = 8 * (int64_t)t0; n < S.Nc; n += kStride) {
-    float d0[8], d1[8];
-    values(n, d0, d1);
-    put(n, d0);
-    if (GATED) put(S.Nc + n, d1);
+  if constexpr (IT > 0) {
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int64_t n = first + 4096 * it;
+      if (n >= S.Nc) continue;
+      put(n, d[0][it]);
+      if (GATED) put(S.Nc + n, d[kMat - 1][it]);
+    }
+  } else {
+    for (int64_t n = first; n < S.Nc; n += 4096) {
+      values(n, d[0][0], d[kMat - 1][0]);
+      put(n, d[0][0]);
+      if (GATED) put(S.Nc + n, d[kMat - 1][0]);
+    }
   }
 }
 
@@ -382,7 +418,7 @@ __global__ __launch_bounds__(BM == 256 ? 512 : 256) void grad_gemm_kernel(
   // wave waited there for its fragments). Nothing is conditional (the last step loads the slice's
   // last step again and writes a stage nobody reads): behind a branch the compiler has to wait for
   // the newest loads before it uses the older ones. 4096 rows, 2 x 11008 x 4096: 1285 us without
-  // any of this, 1040 without branches, 840 with the pieces, HALFTIME with the barrier in the middle.
+  // any of this, 1040 without branches, 840 with the pieces, 800 with the barrier in the middle.
   constexpr int kH = MBLK * NBLK, kPer = (kPieces + kH - 1) / kH;
   const int last = s1 - 1;
   const char* pa = smem + vg * kP + mq * RM * 64;
@@ -547,18 +583,21 @@ static hipError_t grad(const uint16_t* dY, const GatedSaved& V, int act, const G
   uint16_t* lo = reinterpret_cast<uint16_t*>(ws + p.off_lo);
   float* part = p.S > 1 ? reinterpret_cast<float*>(ws + p.off_part) : nullptr;
   hipError_t e;
-  // a wave per row once the rows fill the CUs, eight waves per row below
-#define AWQ_GR(ACT_)                                                                              \
-  do {                                                                                            \
-    if (M >= 1024)                                                                                \
-      grad_rows_kernel<GATED, ACT_, 1><<<(unsigned)((M + 3) / 4) + kParts, 256, 0, stream>>>(     \
-          dY, V, W, S, (int)(K / G), hi, lo, unscale, pmax);                                                          \
-    else                                                                                          \
-      grad_rows_kernel<GATED, ACT_, 8><<<(unsigned)M + kParts, 512, 0, stream>>>(                 \
-          dY, V, W, S, (int)(K / G), hi, lo, unscale, pmax);                                      \
+#define AWQ_GR1(ACT_, IT_)                                                           \
+  grad_rows_kernel<GATED, ACT_, IT_><<<(unsigned)M + kParts, 512, 0, stream>>>(      \
+      dY, V, W, S, (int)(K / G), hi, lo, unscale, pmax)
+#define AWQ_GR(ACT_)                                                                 \
+  do {                                                                               \
+    if (p.Nc <= 4096) AWQ_GR1(ACT_, 1);                                              \
+    else if (p.Nc <= 2 * 4096) AWQ_GR1(ACT_, 2);                                     \
+    else if (p.Nc <= 3 * 4096) AWQ_GR1(ACT_, 3);                                     \
+    else if (p.Nc <= 5 * 4096) AWQ_GR1(ACT_, 5);                                     \
+    else if (p.Nc <= 7 * 4096) AWQ_GR1(ACT_, 7);                                     \
+    else AWQ_GR1(ACT_, 0);                                                           \
   } while (0)
   if (!GATED || act == kSilu) AWQ_GR(kSilu); else AWQ_GR(kGelu);
 #undef AWQ_GR
+#undef AWQ_GR1
   if ((e = hipGetLastError()) != hipSuccess) return e;
   grad_steps_kernel<ZP><<<(unsigned)(p.C / 32), 256, 0, stream>>>(W, S, (int)(K / G), pmax, st, sub,
                                                                   col);

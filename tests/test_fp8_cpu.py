@@ -27,7 +27,7 @@ def refused(fn, good, cases):
 def test_quantize_refuses(lib):
     good = [P, 1, 4, 256, 256, 1, P, P, P, None]
     refused(lib.awq_fp8_quantize, good, [
-        (0, None, NULL), (6, None, NULL), (7, None, NULL), (8, None, NULL), (1, 3, DTYPE),
+        (0, None, NULL), (6, None, NULL), (7, None, NULL), (1, 3, DTYPE),
         (1, -1, DTYPE), (2, 0, SHAPE), (2, -1, SHAPE), (2, (1 << 24) + 1, SHAPE), (3, 0, SHAPE),
         (3, 8, SHAPE), (3, 250, SHAPE), (4, 248, SHAPE), (4, 257, SHAPE), (5, 0, CONFIG),
         (5, 64, CONFIG), (0, P + 8, SHAPE), (6, P + 4, SHAPE), (7, P + 2, SHAPE)])

@@ -66,10 +66,11 @@ def wide(m, k, dtype, seed):
 def test_quantize_bit_exact(awq, dtype, rows, m, k):
     x = wide(m, k, dtype, m + k)
     say("fp8_quantize", dtype, (m, k), "rows", rows)
-    r = awq.fp8_quantize(x.cuda(), block_rows=rows)
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    r = awq.fp8_quantize(x.cuda(), block_rows=rows, flags=flags)
     codes, scales = ref.quantize(x.float().numpy(), rows)
     same(r, codes, scales)
-    assert int(r.flags.item()) == 0
+    assert int(flags.item()) == 0
 
 
 def test_quantize_every_rounding_of_e4m3(awq):
@@ -106,10 +107,11 @@ def test_quantize_nonfinite_and_extremes(awq, dtype, rows):
     x[6, 0] = torch.finfo(dtype).max
     x[7, 130] = -torch.finfo(dtype).max
     say("fp8_quantize nonfinite", dtype, rows)
-    r = awq.fp8_quantize(x.cuda(), block_rows=rows)
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    r = awq.fp8_quantize(x.cuda(), block_rows=rows, flags=flags)
     codes, scales = ref.quantize(x.float().numpy(), rows)
     same(r, codes, scales)
-    assert int(r.flags.item()) == 1               # AWQ_FLAG_NONFINITE_X
+    assert int(flags.item()) == 1               # AWQ_FLAG_NONFINITE_X
 
 
 def test_quantize_strided_view_and_stream(awq):

@@ -80,11 +80,12 @@ def test_gated_ckpt(awq, m, n, k, group, zp, act):
     a = np.random.default_rng(m + n + k).standard_normal((m, k)).astype(np.float16)
     w, z = on_gpu(gate, up)
     say("w4a16_gated_ckpt", (m, n, k), group, zp, act, awq.w4a16_gated_workspace_bytes(m, n, k, True))
-    r = awq.w4a16_gated_ckpt(dev(a), *w, group=group, act=act, **z)
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    r = awq.w4a16_gated_ckpt(dev(a), *w, group=group, act=act, flags=flags, **z)
     g, eg, u, eu, h, eh = ref.gated(a.astype(np.float64), ref.unpack(*gate, group),
                                     ref.unpack(*up, group), group, act)
     check(host(r.H), h, eh)
-    assert int(r.flags.item()) == 0
+    assert int(flags.item()) == 0
     for q, s, x, ex in ((r.g8, r.g_scales, g, eg), (r.u8, r.u_scales, u, eu)):
         s = host(s)
         pad = ((0, 0), (0, -n % 128))
@@ -126,8 +127,10 @@ def test_gated_nonfinite_rows(awq, m):
     w, z = on_gpu(gate, up)
     h = host(awq.w4a16_gated(dev(a), *w, **z))
     assert np.isnan(h[0]).all() and np.isfinite(h[1:]).all()
-    r = awq.w4a16_gated_ckpt(dev(a), *w, **z)
-    assert int(r.flags.item()) == 1 << 11
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    r = awq.w4a16_gated_ckpt(dev(a), *w, flags=flags, **z)
+    assert int(flags.item()) == 1 << 11
+    awq.w4a16_gated_ckpt(dev(a), *w, **z)          # unflagged
     assert np.isnan(host(r.g8.float())[0]).all() and np.isfinite(host(r.g8.float())[1:]).all()
     assert np.all(host(r.g_scales)[0] == 1)
 
