@@ -281,8 +281,7 @@ __global__ __launch_bounds__(256) void fp8_sum_slices_kernel(const float* __rest
                                                              uint16_t* __restrict__ Y) {
   const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (e >= MN) return;
-  floatx4 t = *reinterpret_cast<const floatx4*>(P + e);   // within the padded slice
-  for (int j = 1; j < S; ++j) t = t + *reinterpret_cast<const floatx4*>(P + j * stride + e);
+  const floatx4 t = sum_slices(P + e, S, stride);   // within the padded slice
   if (e + 3 < MN) {
     *reinterpret_cast<uint2*>(Y + e) =
         make_uint2((uint32_t)to16<DT>(t[0]) | ((uint32_t)to16<DT>(t[1]) << 16),

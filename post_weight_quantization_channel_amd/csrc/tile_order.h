@@ -1,4 +1,4 @@
-// Workgroup -> (K slice, row tile, column tile) of a tiled product.
+// Workgroup -> (K slice, row tile, column tile) of a tiled product, and the sum of its K slices.
 #pragma once
 
 #include "device_common.h"
@@ -27,6 +27,23 @@ __device__ __forceinline__ TileAt tile_order(uint32_t tilesM, uint32_t tilesN) {
   t.slice = __builtin_amdgcn_readfirstlane(slice);
   t.tn = __builtin_amdgcn_readfirstlane(tn);
   t.tm = __builtin_amdgcn_readfirstlane(band * BAND + (in_band - tn * bh));
+  return t;
+}
+
+// Four values of S slices, `stride` floats apart, added in slice order; eight slices' loads in
+// flight.
+__device__ __forceinline__ floatx4 sum_slices(const float* P, int S, int64_t stride) {
+  constexpr int kC = 8;
+  floatx4 t = floatx4{0.f, 0.f, 0.f, 0.f};
+  for (int j0 = 0; j0 < S; j0 += kC) {
+    floatx4 v[kC];
+#pragma unroll
+    for (int u = 0; u < kC; ++u)
+      v[u] = *reinterpret_cast<const floatx4*>(P + (j0 + u < S ? j0 + u : 0) * stride);
+#pragma unroll
+    for (int u = 0; u < kC; ++u)
+      if (j0 + u < S) t = (j0 + u == 0) ? v[u] : t + v[u];
+  }
   return t;
 }
 

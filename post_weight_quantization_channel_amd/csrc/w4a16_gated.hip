@@ -609,12 +609,7 @@ __global__ __launch_bounds__(256) void w4a16_gated_finish_kernel(
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const float* p = P + (r * M + row) * Np + n;
-    floatx4 a = *reinterpret_cast<const floatx4*>(p), c = *reinterpret_cast<const floatx4*>(p + 4);
-    for (int j = 1; j < S; ++j) {
-      p += 2 * M * Np;
-      a = a + *reinterpret_cast<const floatx4*>(p);
-      c = c + *reinterpret_cast<const floatx4*>(p + 4);
-    }
+    const floatx4 a = sum_slices(p, S, 2 * M * Np), c = sum_slices(p + 4, S, 2 * M * Np);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       v[r][t] = n + t < N ? a[t] : 0.0f;

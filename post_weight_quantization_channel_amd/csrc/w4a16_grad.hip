@@ -39,23 +39,30 @@ constexpr int kParts = 64;        // parts of n whose largest steps are found si
 constexpr int kMaxGroups = 512;   // K <= 32768, groups of 64
 
 // ---- steps ----------------------------------------------------------------------------------
-// Part `part` of `kParts`: pmax[part][group] = the largest |step| (fp32 bits) of its channels, both
-// matrices. Called by a whole workgroup.
+// Part `part` of `kParts`: pmax[group][part] = the largest |step| (fp16 bits, which order like the
+// numbers) of its channels, both matrices. Called by a workgroup of 512 threads, `wide` (a power of
+// two) of which hold the groups of one channel.
 __device__ __forceinline__ void grad_step_maxima(const GatedWeights& W, const GradShape& S,
                                                  int matrices, int groups, int part,
                                                  uint32_t* __restrict__ pmax, uint32_t* lds) {
-  for (int g = threadIdx.x; g < groups; g += blockDim.x) lds[g] = 0u;
+  const int wide = groups > 256 ? 512 : groups > 128 ? 256 : groups > 64 ? 128 : groups > 32 ? 64 : 32;
+  const int g = threadIdx.x & (wide - 1), r0 = threadIdx.x / wide, rows = 512 / wide;
+  lds[threadIdx.x] = 0u;
   __syncthreads();
   const int64_t per = (S.N + kParts - 1) / kParts;
-  const int64_t n0 = per * part < S.N ? per * part : S.N;
+  const int64_t n0 = per * part;
   const int64_t n1 = n0 + per < S.N ? n0 + per : S.N;
-  for (int mat = 0; mat < matrices; ++mat) {
-    const uint16_t* s = W.s[mat] + n0 * groups;
-    for (int e = threadIdx.x; e < (int)((n1 - n0) * groups); e += blockDim.x)
-      atomicMax(&lds[e % groups], __float_as_uint(fabsf(h2f(s[e]))));
+  uint32_t mx = 0u;
+  if (g < groups) {
+    for (int mat = 0; mat < matrices; ++mat) {
+      const uint16_t* s = W.s[mat] + g;
+#pragma unroll 8
+      for (int64_t n = n0 + r0; n < n1; n += rows) mx = max(mx, (uint32_t)(s[n * groups] & 0x7FFFu));
+    }
+    atomicMax(&lds[g], mx);
   }
   __syncthreads();
-  for (int g = threadIdx.x; g < groups; g += blockDim.x) pmax[part * groups + g] = lds[g];
+  if ((int)threadIdx.x < groups) pmax[threadIdx.x * kParts + part] = lds[threadIdx.x];
 }
 
 // One workgroup: 32 channels of the contraction, up to 128 groups of columns at a time (read along
@@ -84,14 +91,17 @@ __global__ __launch_bounds__(256) void grad_steps_kernel(GatedWeights W, GradSha
       tile[r * kTG + g] = W.s[mat][at];
       if (ZP) ztile[r * kTG + g] = W.z[mat][at];
     }
-    if ((int)threadIdx.x < ng) {
-      const int g = threadIdx.x;
-      uint32_t u = 0u;
-#pragma unroll 16
-      for (int p = 0; p < kParts; ++p) u = max(u, pmax[p * groups + g0 + g]);
+    // 16 lanes per group: four parts each, then the maximum over the lanes
+    for (int g = threadIdx.x >> 4; g < ng; g += 16) {
+      const uint4 p = *reinterpret_cast<const uint4*>(pmax + (g0 + g) * kParts + 4 * (threadIdx.x & 15));
+      const uint32_t bits = max(max(p.x, p.y), max(p.z, p.w));
+      const float top = group_absmax<16>(h2f((uint16_t)bits));
+      const uint32_t u = __float_as_uint(top);
       // the power of two at or above the largest step; 1 for 0 and for a non-finite step
-      expo[g] = (u == 0u || u >= 0x7F800000u) ? 127u : (u + 0x7FFFFFu) >> 23;
-      if (blockIdx.x == 0) colscale[g0 + g] = __uint_as_float(expo[g] << 23);
+      if ((threadIdx.x & 15) == 0) {
+        expo[g] = (u == 0u || u >= 0x7F800000u) ? 127u : (u + 0x7FFFFFu) >> 23;
+        if (blockIdx.x == 0) colscale[g0 + g] = __uint_as_float(expo[g] << 23);
+      }
     }
     __syncthreads();
     const int r = threadIdx.x & 31;
@@ -524,8 +534,7 @@ __global__ __launch_bounds__(256) void grad_finish_kernel(const float* __restric
   const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;   // K % 128 == 0: one row
   if (e >= MK) return;
   const int64_t m = e / S.K, k = e - m * S.K;
-  floatx4 t = *reinterpret_cast<const floatx4*>(P + e);
-  for (int j = 1; j < slices; ++j) t = t + *reinterpret_cast<const floatx4*>(P + j * MK + e);
+  const floatx4 t = sum_slices(P + e, slices, MK);
   const float us = unscale[m] * colscale[k / group];
   float v[4];
 #pragma unroll
@@ -548,9 +557,10 @@ GradPlan w4a16_grad_plan(int64_t M, int64_t N, int64_t K, int group, bool gated,
   p.tm = (M + p.bm - 1) / p.bm;
   p.tk = (K + 2 * group - 1) / (2 * group);
   const int64_t T = p.C / 32, tiles = p.tm * p.tk;
-  const int64_t want = p.bm == 256 ? 256 : 512;      // one large workgroup per CU, or two small
+  // one large workgroup per CU, or two small; at least 8 or 4 steps each
+  const int64_t want = p.bm == 256 ? 256 : 512, least = p.bm == 256 ? 8 : 4;
   int64_t S = want / tiles;
-  S = S > T / 8 ? T / 8 : S;
+  S = S > T / least ? T / least : S;
   S = S < 1 ? 1 : S;
   p.steps = (T + S - 1) / S;
   p.S = (T + p.steps - 1) / p.steps;
