@@ -135,8 +135,7 @@ __global__ __launch_bounds__(64 * kSkWaves) void fp8_skinny_kernel(
 
 // Tile BM (activation rows) x BN (weight rows), one scale block of K per step, WM x WN waves. The
 // tiles of a step (rows of 128 bytes) are moved into one of two LDS stages by the buffer unit
-// while the other stage is multiplied: step b waits for its own loads, passes a barrier (everyone's
-// have landed, and the other stage's last reader is done), issues step b + 1's and computes.
+// while the other stage is multiplied.
 // Chunk c (16 bytes) of LDS row r sits at position c ^ ((r >> 1) & 7): the 16 rows a fragment read
 // touches at once then cover all 64 banks. The step's activation scales (one per row, gathered)
 // go to LDS the same way. Rows past M or N, and channels past K, read as zeros.
@@ -213,42 +212,86 @@ __global__ __launch_bounds__(64 * WM * WN) void fp8_tiled_kernel(
   for (int i = 0; i < MB; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[i][j] = floatx4{0.f, 0.f, 0.f, 0.f};
-  auto compute = [&](int st, float swv) {
-    const char* base = smem + st * kStage;
-    const float* srow = reinterpret_cast<const float*>(base + kTiles) + wm * MB * 16 + li;
-    const char* arow = base + wm * MB * 16 * 128;
-    const char* wrow = base + (BM + wn * NB * 16) * 128;
-    intx8 wf[NB];
+  // Step b: the matrix instructions of one 16-row block after another. While block i's run, block
+  // i + 2's fragment is read (one block ahead is less than an LDS read takes) and block i - 1's
+  // results are scaled and added. Two blocks before the end the wave waits for step b + 1's loads
+  // and passes the barrier (its own reads of this stage are done, everyone's loads have landed): the
+  // last blocks' instructions then cover the issue of step b + 2's loads into this stage and the
+  // reads of step b + 1's first fragments.
+  // The last steps load the last block again, so that no wait stands behind a branch.
+  static_assert(MB % 2 == 0, "the fragment registers take turns");
+  intx8 wf[NB], af[2];
+  floatx4 part[NB];           // results not yet added, and their row block's scale
+  float psc = 0.0f, asc[2];   // scales of the blocks in af
 #pragma unroll
-    for (int j = 0; j < NB; ++j) wf[j] = frag(wrow + j * 16 * 128);
+  for (int j = 0; j < NB; ++j) part[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+  auto wrows = [&](int st) { return smem + st * kStage + (BM + wn * NB * 16) * 128; };
+  auto arows = [&](int st) { return smem + st * kStage + wm * MB * 16 * 128; };
+  auto scale_at = [&](int st, int i) {
+    return reinterpret_cast<const float*>(smem + st * kStage + kTiles)[(wm * MB + i) * 16 + li];
+  };
+  auto step = [&](int b, int st, float sw0, float sw1) {
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-      const intx8 af = frag(arow + i * 16 * 128);
-      const float sc = srow[i * 16] * swv;
+      const int ip = i == 0 ? MB - 1 : i - 1;
+      if (i == MB - 2) {
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+        __syncthreads();
+        issue(b + 2 < b1 ? b + 2 : b1 - 1, st);
+        issue_scales(b + 2 < b1 ? b + 2 : b1 - 1, st);
+      }
+      float sc;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
-        const floatx4 p = mfma_fp8(wf[j], af, floatx4{0.f, 0.f, 0.f, 0.f});
+        const floatx4 p = mfma_fp8(wf[j], af[i & 1], floatx4{0.f, 0.f, 0.f, 0.f});
+        if (i == MB - 1) wf[j] = frag(wrows(st ^ 1) + j * 16 * 128);
+        if (j == NB - 1) {   // the block's fragment is used: read the next but one
+          sc = asc[i & 1];
+          const int st2 = i + 2 < MB ? st : st ^ 1, i2 = i + 2 < MB ? i + 2 : i + 2 - MB;
+          af[i & 1] = frag(arows(st2) + i2 * 16 * 128);
+          asc[i & 1] = scale_at(st2, i2) * (i + 2 < MB ? sw0 : sw1);
+        }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], sc, acc[i][j][r]);
+        for (int r = 0; r < 4; ++r)
+          acc[ip][j][r] = __builtin_fmaf(part[j][r], psc, acc[ip][j][r]);
+        // here, not later: the sums would otherwise pile up behind the matrix instructions
+        asm volatile("" : "+v"(acc[ip][j]));
+        part[j] = p;
+        __builtin_amdgcn_sched_barrier(0);
       }
+      psc = sc;
     }
   };
-
+  auto weight_scale = [&](int b) { return swr[b < b1 ? b : b1 - 1]; };
   issue(b0, 0);
   issue_scales(b0, 0);
-  float swv = swr[b0];
-  for (int b = b0; b < b1; ++b) {
-    const int st = (b - b0) & 1;
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-    __syncthreads();
-    const float swn = swr[b + 1 < b1 ? b + 1 : b];
-    if (b + 1 < b1) {
-      issue(b + 1, st ^ 1);
-      issue_scales(b + 1, st ^ 1);
-    }
-    compute(st, swv);
-    swv = swn;
+  issue(b0 + 1 < b1 ? b0 + 1 : b0, 1);
+  issue_scales(b0 + 1 < b1 ? b0 + 1 : b0, 1);
+  float sw0 = weight_scale(b0), sw1 = weight_scale(b0 + 1);
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < NB; ++j) wf[j] = frag(wrows(0) + j * 16 * 128);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    af[i] = frag(arows(0) + i * 16 * 128);
+    asc[i] = scale_at(0, i) * sw0;
   }
+  int b = b0;
+  for (; b + 1 < b1; b += 2) {
+    const float sw2 = weight_scale(b + 2), sw3 = weight_scale(b + 3);
+    step(b, 0, sw0, sw1);
+    step(b + 1, 1, sw1, sw2);
+    sw0 = sw2;
+    sw1 = sw3;
+  }
+  if (b < b1) step(b, 0, sw0, sw1);
+#pragma unroll
+  for (int j = 0; j < NB; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      acc[MB - 1][j][r] = __builtin_fmaf(part[j][r], psc, acc[MB - 1][j][r]);
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));   // no load may land in LDS that is no longer ours
 
   // ---- store ----------------------------------------------------------------------------------
 #pragma unroll
