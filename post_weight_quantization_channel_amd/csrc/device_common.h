@@ -404,17 +404,33 @@ __device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t num_bytes
   return r;
 }
 
-// Plain loads through such a descriptor (16 and 4 bytes at byte offset voff; zeros past its range).
+// Plain loads through such a descriptor, at byte offset voff (per lane) + soff (wave-uniform); zeros
+// past its range.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(rsrc_t r) {
   const uint64_t base = (uint64_t)(uint32_t)r[0] | ((uint64_t)(uint32_t)r[1] << 32);
   return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, r[2], r[3]);
 }
-__device__ __forceinline__ uint4 buffer_load16(rsrc_t r, uint32_t voff) {
-  const auto v = __builtin_amdgcn_raw_buffer_load_b128(buffer_of(r), (int)voff, 0, 0);
+__device__ __forceinline__ uint4 buffer_load16(rsrc_t r, uint32_t voff, uint32_t soff = 0u) {
+  const auto v = __builtin_amdgcn_raw_buffer_load_b128(buffer_of(r), (int)voff, (int)soff, 0);
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
-__device__ __forceinline__ uint32_t buffer_load4(rsrc_t r, uint32_t voff) {
-  return __builtin_amdgcn_raw_buffer_load_b32(buffer_of(r), (int)voff, 0, 0);
+__device__ __forceinline__ uint2 buffer_load8(rsrc_t r, uint32_t voff, uint32_t soff = 0u) {
+  const auto v = __builtin_amdgcn_raw_buffer_load_b64(buffer_of(r), (int)voff, (int)soff, 0);
+  return make_uint2(v[0], v[1]);
+}
+__device__ __forceinline__ uint32_t buffer_load4(rsrc_t r, uint32_t voff, uint32_t soff = 0u) {
+  return __builtin_amdgcn_raw_buffer_load_b32(buffer_of(r), (int)voff, (int)soff, 0);
+}
+__device__ __forceinline__ uint32_t buffer_load2(rsrc_t r, uint32_t voff, uint32_t soff = 0u) {
+  return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(buffer_of(r), (int)voff, (int)soff, 0);
+}
+__device__ __forceinline__ uint32_t buffer_load1(rsrc_t r, uint32_t voff, uint32_t soff = 0u) {
+  return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(buffer_of(r), (int)voff, (int)soff, 0);
+}
+
+// and a store, dropped past the range
+__device__ __forceinline__ void buffer_store4(rsrc_t r, uint32_t voff, uint32_t soff, uint32_t v) {
+  __builtin_amdgcn_raw_buffer_store_b32(v, buffer_of(r), (int)voff, (int)soff, 0);
 }
 
 // LDS byte address of a __shared__ object (for M0 below).

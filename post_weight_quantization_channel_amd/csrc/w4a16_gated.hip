@@ -180,24 +180,25 @@ __global__ __launch_bounds__(64 * kGvWaves) void w4a16_gated_gemv_kernel(
 
 namespace {
 
-// The fragment of one word of 8 codes: exact fp16 values in natural order. Byte j of the word
-// (channels 2j, 2j + 1) is spread to bytes 0 and 2; with the exponent bits around them the pair is
+// Pair j (channels 2j, 2j + 1) of a word's 8 codes as exact fp16 values: byte j is spread to bytes 0
+// and 2; with the exponent bits around them, and bit 3 of signed codes flipped, the pair is
 // (1024 + u, 1024 + 16 u'), and one packed fma with (1, 1/16) and -(1024 + zc, 64 + zc) gives
-// (c, c'); zc = 8 for signed codes (biased by the xor) or the zero point. mul = (1, 1/16); with
-// mul and nsub zero the values are zero.
+// (c, c'); zc = 8 for signed codes (u = c + 8) or the zero point.
 template <bool ZP>
-__device__ __forceinline__ half8_t decode8(uint32_t w, uint32_t magic, half2_t mul, half2_t nsub) {
-  const uint32_t x = ZP ? w : (w ^ 0x88888888u);
+__device__ __forceinline__ void decode_pair(uint32_t w, int j, half2_t nsub, half8_t& f) {
+  constexpr uint32_t kExp = ZP ? 0x64006400u : 0x64806408u;
+  const uint32_t t = __builtin_amdgcn_perm(w, w, 0x0C000C00u | (uint32_t)j | ((uint32_t)j << 16));
+  const half2_t q = __builtin_elementwise_fma(
+      __builtin_bit_cast(half2_t, (t & 0x00F0000Fu) ^ kExp),
+      half2_t{(_Float16)1.0f, (_Float16)0.0625f}, nsub);
+  f[2 * j] = q[0];
+  f[2 * j + 1] = q[1];
+}
+template <bool ZP>
+__device__ __forceinline__ half8_t decode8(uint32_t w, half2_t nsub) {
   half8_t f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t t = __builtin_amdgcn_perm(x, x, 0x0C000C00u | (uint32_t)j | ((uint32_t)j << 16));
-    const uint32_t bits = (t & 0x00F0000Fu) | magic;
-    const half2_t q = __builtin_elementwise_fma(
-        __builtin_bit_cast(half2_t, bits), mul, nsub);
-    f[2 * j] = q[0];
-    f[2 * j + 1] = q[1];
-  }
+  for (int j = 0; j < 4; ++j) decode_pair<ZP>(w, j, nsub, f);
   return f;
 }
 __device__ __forceinline__ half2_t decode_nsub(float zc) {
@@ -245,8 +246,6 @@ __global__ __launch_bounds__(64 * kSkWaves) void w4a16_gated_skinny_kernel(
   const uint16_t* ar[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) ar[t] = A + (16 * t + li < M ? 16 * t + li : M - 1) * K;
-  uint32_t magic = 0x64006400u;
-  asm volatile("" : "+v"(magic));   // held in a register: the mask-and-insert is one instruction
   floatx4 acc[2][MT];
 #pragma unroll
   for (int r = 0; r < 2; ++r)
@@ -286,8 +285,7 @@ __global__ __launch_bounds__(64 * kSkWaves) void w4a16_gated_skinny_kernel(
         for (int t = 0; t < MT; ++t) part[t] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kk = h * 4 / kG; kk < (h + 1) * 4 / kG; ++kk) {
-          const half8_t wf = decode8<ZP>(b.w[r][kk], magic,
-                                         half2_t{(_Float16)1.0f, (_Float16)0.0625f}, nsub);
+          const half8_t wf = decode8<ZP>(b.w[r][kk], nsub);
 #pragma unroll
           for (int t = 0; t < MT; ++t)
             part[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b.a[t][kk], wf, part[t], 0, 0, 0);
@@ -346,7 +344,7 @@ __global__ __launch_bounds__(64 * kSkWaves) void w4a16_gated_skinny_kernel(
 // at a group's start they are multiplied by (last step / this step), and by the last step at the
 // end. Each such factor is within 2^-22 of the quotient. A group whose step is 0 decodes to zeros
 // and keeps the step before it.
-// Rows past M read as zeros, output channels past N read channel N - 1; neither is stored.
+// Rows past M and output channels past N read as zeros; neither is stored.
 struct GatedOut {
   uint16_t* H;
   uint8_t *g8, *u8;        // nullptr: not kept
@@ -386,17 +384,18 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
                            (uint32_t)(r0 * K * 2) + (uint32_t)b * 256u);
     }
   };
-  // column blocks t = 2 matrix + half: output channels n0 + 32 wave + 16 half + li. Byte offsets
-  // of the lane's rows from the tile's first row (128 rows of at most 16 KiB).
-  const char *qb[2], *sb[2], *zb[2];
+  // column blocks t = 2 matrix + half: output channels n0 + 32 wave + 16 half + li, read through buffer
+  // descriptors that start at the tile's first channel (a lane's offsets then never change, and
+  // channels past N read as zeros)
+  const uint32_t nrows = (uint32_t)(N - n0 < kTN ? N - n0 : kTN);
+  rsrc_t rq[2], rst[2], rz[2];
   uint32_t qoff[2], goff[2];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    qb[r] = reinterpret_cast<const char*>(W.q[r] + n0 * (K / 8));
-    sb[r] = reinterpret_cast<const char*>(W.s[r] + n0 * (K / GS));
-    zb[r] = ZP ? reinterpret_cast<const char*>(W.z[r] + n0 * (K / GS)) : nullptr;
-    const int64_t n = 32 * wave + 16 * r + li;
-    const uint32_t row = (uint32_t)(n0 + n < N ? n : N - 1 - n0);
+    rq[r] = make_rsrc(W.q[r] + n0 * (K / 8), nrows * (uint32_t)(K / 2));
+    rst[r] = make_rsrc(W.s[r] + n0 * (K / GS), nrows * (uint32_t)(K / GS) * 2u);
+    if (ZP) rz[r] = make_rsrc(W.z[r] + n0 * (K / GS), nrows * (uint32_t)(K / GS));
+    const uint32_t row = (uint32_t)(32 * wave + 16 * r + li);
     qoff[r] = row * (uint32_t)(K / 2) + (uint32_t)lg * (GS == 128 ? 16u : 8u);
     goff[r] = row * (uint32_t)(K / GS);
   }
@@ -404,26 +403,23 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
     uint32_t w[4][4], st[4], z[4];   // st, z: groups of 64 hold both groups' values
   };
   auto load_codes = [&](int b, Codes& c) {
+    const uint32_t qs = (uint32_t)b * 64u, gs = (uint32_t)b * (uint32_t)kG;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const char* q = qb[t >> 1] + (uint32_t)b * 64u;
+      const int r = t >> 1, h = t & 1;
       if (GS == 128) {
-        const uint4 v = *reinterpret_cast<const uint4*>(q + qoff[t & 1]);
+        const uint4 v = buffer_load16(rq[r], qoff[h], qs);
         c.w[t][0] = v.x; c.w[t][1] = v.y; c.w[t][2] = v.z; c.w[t][3] = v.w;
-        c.st[t] = *reinterpret_cast<const uint16_t*>(sb[t >> 1] + (uint32_t)b * 2u + 2u * goff[t & 1]);
-        if (ZP) c.z[t] = *reinterpret_cast<const uint8_t*>(zb[t >> 1] + (uint32_t)b + goff[t & 1]);
+        c.st[t] = buffer_load2(rst[r], 2u * goff[h], 2u * gs);
+        if (ZP) c.z[t] = buffer_load1(rz[r], goff[h], gs);
       } else {
-        const uint2 v = *reinterpret_cast<const uint2*>(q + qoff[t & 1]);
-        const uint2 x = *reinterpret_cast<const uint2*>(q + qoff[t & 1] + 32);
+        const uint2 v = buffer_load8(rq[r], qoff[h], qs), x = buffer_load8(rq[r], qoff[h] + 32u, qs);
         c.w[t][0] = v.x; c.w[t][1] = v.y; c.w[t][2] = x.x; c.w[t][3] = x.y;
-        c.st[t] = *reinterpret_cast<const uint32_t*>(sb[t >> 1] + (uint32_t)b * 4u + 2u * goff[t & 1]);
-        if (ZP)
-          c.z[t] = *reinterpret_cast<const uint16_t*>(zb[t >> 1] + (uint32_t)b * 2u + goff[t & 1]);
+        c.st[t] = buffer_load4(rst[r], 2u * goff[h], 2u * gs);
+        if (ZP) c.z[t] = buffer_load2(rz[r], goff[h], gs);
       }
     }
   };
-  uint32_t magic = 0x64006400u;
-  asm volatile("" : "+v"(magic));
   floatx4 acc[4][MB];   // [column block][16-row block]
   float prev[4];        // the step the accumulators are divided by
 #pragma unroll
@@ -436,16 +432,15 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
     const char* sa = smem + st * kStage;
 #pragma unroll
     for (int h = 0; h < kG; ++h) {
-      half2_t nsub[4], mul[4];
+      half2_t nsub[4];
+      bool none[4];   // a step of 0: the codes are taken as ones that decode to 0
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const float s = h2f((uint16_t)(h == 0 ? c.st[t] & 0xFFFFu : c.st[t] >> 16));
         const float z = ZP ? (float)(GS == 128 ? c.z[t] : h == 0 ? c.z[t] & 0xFFu : c.z[t] >> 8) : 8.0f;
-        const bool none = s == 0.0f;
-        const half2_t zero2 = half2_t{(_Float16)0.0f, (_Float16)0.0f};
-        nsub[t] = none ? zero2 : decode_nsub(z);
-        mul[t] = none ? zero2 : half2_t{(_Float16)1.0f, (_Float16)0.0625f};
-        const float now = none ? prev[t] : s;
+        none[t] = s == 0.0f;
+        nsub[t] = decode_nsub(ZP && none[t] ? 0.0f : z);
+        const float now = none[t] ? prev[t] : s;
         const float ratio = prev[t] * __builtin_amdgcn_rcpf(now);
         prev[t] = now;
 #pragma unroll
@@ -458,7 +453,7 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
         const int ch = chunk_of<GS>(lg, kk);
         half8_t wf[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) wf[t] = decode8<ZP>(c.w[t][kk], magic, mul[t], nsub[t]);
+        for (int t = 0; t < 4; ++t) wf[t] = decode8<ZP>(none[t] ? 0u : c.w[t][kk], nsub[t]);
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
           const half8_t af =
@@ -496,18 +491,22 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
       for (int e = 0; e < 4; ++e) acc[t][i][e] *= prev[t];
 
   // a lane holds, for block i and element e, row m0 + 16 i + 4 lg + e of its output channels
-  if (partials) {   // [slice][matrix][M][Np], Np = whole tiles
-    float* P = partials + (int64_t)at.slice * 2 * M * Np;
+  if (partials) {   // [slice][matrix][M][Np], Np = whole tiles; stores past the last row are dropped
+    const uint32_t rows = (uint32_t)(M - m0 < TM ? M - m0 : TM), ld = (uint32_t)Np * 4u;
+    const uint32_t off = (uint32_t)(4 * lg) * ld + (uint32_t)(32 * wave + li) * 4u;
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int r = 0; r < 2; ++r) {
+      const rsrc_t rp = make_rsrc(partials + (((int64_t)at.slice * 2 + r) * M + m0) * Np + n0,
+                                  rows * ld - (uint32_t)n0 * 4u);
 #pragma unroll
-      for (int i = 0; i < MB; ++i)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int64_t m = m0 + 16 * i + 4 * lg + e;
-          if (m < M)
-            P[((t >> 1) * M + m) * Np + n0 + 32 * wave + 16 * (t & 1) + li] = acc[t][i][e];
-        }
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            buffer_store4(rp, off + 64u * h, (uint32_t)(16 * i + e) * ld,
+                          __float_as_uint(acc[2 * r + h][i][e]));
+    }
     return;
   }
   __syncthreads();   // the last step's reads of the stages are done
