@@ -487,8 +487,9 @@ __global__ __launch_bounds__(BM == 256 ? 512 : 256) void grad_gemm_kernel(
   // ---- store: a lane's block j holds column 8 w + i8, w = lane % WPG -------------------------
   const int64_t kl = k0 + vg * G + 8 * (l32 % WPG) + l32 / WPG;   // of block 0; + 32 / WPG per block
   const int64_t ml = m0 + mq * RM + 4 * lh;
-  if (kl >= S.K) return;   // a whole group of columns: K % G == 0
+  const bool live = k0 + vg * G < S.K;   // a whole group of columns: K % G == 0
   if (partials) {
+    if (!live) return;
     float* P = partials + (int64_t)at.slice * S.M * S.K + kl;
 #pragma unroll
     for (int i = 0; i < MBLK; ++i)
@@ -502,25 +503,40 @@ __global__ __launch_bounds__(BM == 256 ? 512 : 256) void grad_gemm_kernel(
       }
     return;
   }
-  const float cs = colscale[kl / G];
+  // Through LDS, 32 rows of the wave's columns at a time (a region per wave), so that a row's columns
+  // leave as whole lines.
+  constexpr int kPitch = 2 * G + 16;
+  static_assert(kWaves * 32 * kPitch <= 2 * kStage, "the regions fit the stages");
+  const float cs = live ? colscale[kl / G] : 1.0f;
   float sv[NBLK];
 #pragma unroll
-  for (int j = 0; j < NBLK; ++j) sv[j] = s16 ? h2f(s16[kl + (32 / WPG) * j]) : 1.0f;
+  for (int j = 0; j < NBLK; ++j) sv[j] = live && s16 ? h2f(s16[kl + (32 / WPG) * j]) : 1.0f;
+  __syncthreads();   // the stages are read
+  if (!live) return;
+  char* reg = smem + wave * 32 * kPitch;
 #pragma unroll
-  for (int i = 0; i < MBLK; ++i)
+  for (int i = 0; i < MBLK; ++i) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const int64_t m = ml + 32 * i + 8 * (e >> 2) + (e & 3);
-      if (m < S.M) {
-        const float us = unscale[m] * cs;
+      const int r = 8 * (e >> 2) + (e & 3) + 4 * lh;
+      const int64_t m = m0 + mq * RM + 32 * i + r;
+      const float us = unscale[m < S.M ? m : S.M - 1] * cs;
 #pragma unroll
-        for (int j = 0; j < NBLK; ++j) {
-          float v = acc[i][j][e] * us;
-          if (s16) v = v / sv[j];
-          dA[m * S.K + kl + (32 / WPG) * j] = f2h(v);
-        }
+      for (int j = 0; j < NBLK; ++j) {
+        float v = acc[i][j][e] * us;
+        if (s16) v = v / sv[j];
+        *reinterpret_cast<uint16_t*>(reg + r * kPitch +
+                                     2 * (8 * (l32 % WPG) + l32 / WPG + (32 / WPG) * j)) = f2h(v);
       }
     }
+#pragma unroll
+    for (int e = 0; e < G / 16; ++e) {   // 32 rows of G / 8 chunks of 16 bytes
+      const int x = 64 * e + lane, r = x / (G / 8), c = x % (G / 8);
+      const uint4 v = *reinterpret_cast<const uint4*>(reg + r * kPitch + c * 16);
+      const int64_t m = m0 + mq * RM + 32 * i + r;
+      if (m < S.M) *reinterpret_cast<uint4*>(dA + m * S.K + k0 + vg * G + 8 * c) = v;
+    }
+  }
 }
 
 // dA = round(sum of the slices' partials [slices][M][K] times 2^(f - e) (/ s[k])), slices in order.
