@@ -432,7 +432,7 @@ awq_status awq_act_stats_noalloc(const void* X, awq_dtype xdt, int64_t M, int64_
  * flags    in/out, or NULL: NONFINITE_X (an Inf or NaN, whose code is NaN; the block's scale is
  *          that of its finite values).
  * Errors: AWQ_ERR_NULL, AWQ_ERR_DTYPE, AWQ_ERR_CONFIG (block_rows), AWQ_ERR_SHAPE (sizes, ldx,
- *         misalignment; more than 2^31 blocks of one row).
+ *         misalignment; more than 2^28 - 16 blocks of 1 x 128).
  * ---------------------------------------------------------------------------------------- */
 awq_status awq_fp8_quantize(const void* X, awq_dtype xdt, int64_t M, int64_t K, int64_t ldx,
                             int32_t block_rows, uint8_t* q, float* scales, uint32_t* flags,
@@ -458,7 +458,7 @@ awq_status awq_fp8_dequantize(const uint8_t* q, const float* scales, int64_t M, 
  *          output tiles number fewer than the CUs), which are added in a fixed order. Calls that
  *          share a workspace must not overlap.
  * Errors: AWQ_ERR_NULL, AWQ_ERR_DTYPE, AWQ_ERR_SHAPE (M < 1, N < 1, K < 16, K % 16, K > 2^20,
- *         M N > 2^38, misalignment), AWQ_ERR_WORKSPACE.
+ *         M N > 2^36, misalignment), AWQ_ERR_WORKSPACE.
  * ---------------------------------------------------------------------------------------- */
 size_t awq_fp8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 awq_status awq_fp8_gemm(const uint8_t* A8, const float* a_scales, const uint8_t* W8,
@@ -482,7 +482,7 @@ awq_status awq_fp8_gemm(const uint8_t* A8, const float* a_scales, const uint8_t*
  *          (M > 32 while the tiles leave CUs idle), added in a fixed order. Calls that share a
  *          workspace must not overlap.
  * Errors: AWQ_ERR_NULL, AWQ_ERR_CONFIG (group, act, zeros on one side only), AWQ_ERR_SHAPE (M < 1,
- *         N < 1, K % 128, K > 32768, M N > 2^38, misalignment), AWQ_ERR_WORKSPACE.
+ *         N < 1, K % 128, K > 32768, M N > 2^36, misalignment), AWQ_ERR_WORKSPACE.
  * ---------------------------------------------------------------------------------------- */
 enum { AWQ_ACT_SILU = 0, AWQ_ACT_GELU = 1 };
 typedef struct {
@@ -523,7 +523,7 @@ awq_status w4a16_gated_ckpt(const uint16_t* A, int64_t M, int64_t N, int64_t K, 
  * Arithmetic: dg and du in fp32; the products' operands are fp16(d step) (scaled by powers of two
  * per row and column group) and the exact codes; fp32 sums, in a fixed order; dA rounded once. A
  * row of dH, g or u that holds an Inf or NaN gives a row of dA that is not finite.
- * Errors: as w4a16_gated; AWQ_ERR_SHAPE also when N % 16 != 0.
+ * Errors: as w4a16_gated; AWQ_ERR_SHAPE also when N % 16 != 0 or M > 2^22.
  * ---------------------------------------------------------------------------------------- */
 size_t w4a16_gated_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t group,
                                             int32_t zero_point);
@@ -540,7 +540,8 @@ awq_status w4a16_gated_backward(const uint16_t* dH, const uint8_t* g8, const flo
  *          [M, K], 16-byte aligned; packed arguments as w4a16_gemm.
  * ws       as w4a16_gated_backward, of w4a16_gemm_backward_workspace_bytes(M, N, K, group, zeros
  *          given) bytes. Arithmetic as there.
- * Errors: AWQ_ERR_NULL, AWQ_ERR_CONFIG, AWQ_ERR_SHAPE (as w4a16_gated), AWQ_ERR_WORKSPACE.
+ * Errors: AWQ_ERR_NULL, AWQ_ERR_CONFIG, AWQ_ERR_SHAPE (as w4a16_gated, or M > 2^22),
+ *         AWQ_ERR_WORKSPACE.
  * ---------------------------------------------------------------------------------------- */
 size_t w4a16_gemm_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t group,
                                            int32_t zero_point);

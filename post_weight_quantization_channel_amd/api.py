@@ -455,9 +455,10 @@ class Fp8Result:
 
 
 def _same_device(ref: torch.Tensor, *named) -> None:
+    device = ref.device
     for t, nm in named:
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{nm} must be on {ref.device}")
+        if t is not None and t.device != device:
+            raise ValueError(f"{nm} must be on {device}")
 
 
 def _flags_arg(flags, device):
@@ -510,12 +511,13 @@ def _blocks_shape(M: int, K: int, block_rows: int):
 
 def _fp8_check(q, scales, block_rows, name):
     _dev(q, name)
-    _dev(scales, f"{name} scales")
+    _dev(scales, "the scales of " + name)
     if q.dim() != 2 or q.dtype != FP8:
         raise ValueError(f"{name} must be float8_e4m3fn [rows, columns]")
-    if scales.dtype != torch.float32 or \
-            tuple(scales.shape) != _blocks_shape(q.shape[0], q.shape[1], block_rows):
+    M, K = q.shape
+    if scales.dtype != torch.float32 or scales.shape != _blocks_shape(M, K, block_rows):
         raise ValueError(f"{name}: the scales must be fp32, one per block of {block_rows} x 128")
+    return M, K
 
 
 def fp8_quantize(X: torch.Tensor, block_rows: int = 1,
@@ -537,8 +539,8 @@ def fp8_quantize(X: torch.Tensor, block_rows: int = 1,
     q = torch.empty((M, K), dtype=FP8, device=dev)
     scales = torch.empty(_blocks_shape(M, K, block_rows), dtype=torch.float32, device=dev)
     _launch("awq_fp8_quantize", lib.awq_fp8_quantize, dev,
-        X.data_ptr(), _DT[X.dtype], M, K, X.stride(0) if M > 1 else K, block_rows,
-        q.data_ptr(), scales.data_ptr(), fl)
+            X.data_ptr(), _DT[X.dtype], M, K, X.stride(0) if M > 1 else K, block_rows,
+            q.data_ptr(), scales.data_ptr(), fl)
     return Fp8Result(q, scales, flags)
 
 
@@ -556,7 +558,7 @@ def fp8_dequantize(q: torch.Tensor, scales: torch.Tensor, block_rows: int = 1,
     M, K = q.shape
     out = _out(out, (M, K), dtype, q.device)
     _launch("awq_fp8_dequantize", lib.awq_fp8_dequantize, q.device,
-        q.data_ptr(), scales.data_ptr(), M, K, block_rows, _DT[dtype], out.data_ptr())
+            q.data_ptr(), scales.data_ptr(), M, K, block_rows, _DT[dtype], out.data_ptr())
     return out
 
 
@@ -571,11 +573,9 @@ def fp8_gemm(A8: torch.Tensor, a_scales: torch.Tensor, W8: torch.Tensor, w_scale
     """Y = (A8 a_scales) (W8 w_scales)^T, fp16 or bf16 [M, N], from fp8_quantize's formats: A8 in
     blocks of 1 x 128, W8 [N, K] in blocks of 128 x 128."""
     lib = _lib.load()
-    _fp8_check(A8, a_scales, 1, "A8")
-    _fp8_check(W8, w_scales, 128, "W8")
-    M, K = A8.shape
-    N = W8.shape[0]
-    if W8.shape[1] != K:
+    M, K = _fp8_check(A8, a_scales, 1, "A8")
+    N, KW = _fp8_check(W8, w_scales, 128, "W8")
+    if KW != K:
         raise ValueError("A8 and W8 must have the same number of columns")
     if out_dtype not in (torch.float16, torch.bfloat16):
         raise ValueError("out_dtype must be fp16 or bf16")
@@ -584,9 +584,9 @@ def fp8_gemm(A8: torch.Tensor, a_scales: torch.Tensor, W8: torch.Tensor, w_scale
     out = _out(out, (M, N), out_dtype, dev)
     ws = _scratch(workspace, lib.awq_fp8_gemm_workspace_bytes(M, N, K), dev)
     _launch("awq_fp8_gemm", lib.awq_fp8_gemm, dev,
-        A8.data_ptr(), a_scales.data_ptr(), W8.data_ptr(), w_scales.data_ptr(), M, N, K,
-        _DT[out_dtype], out.data_ptr(), ws.data_ptr() if ws is not None else None,
-        ws.numel() * ws.element_size() if ws is not None else 0)
+            A8.data_ptr(), a_scales.data_ptr(), W8.data_ptr(), w_scales.data_ptr(), M, N, K,
+            _DT[out_dtype], out.data_ptr(), ws.data_ptr() if ws is not None else None,
+            ws.numel() * ws.element_size() if ws is not None else 0)
     return out
 
 
@@ -599,7 +599,7 @@ def _packed_check(x, K, qweight, scales16, zeros, group, name):
     _dev(scales16, f"{name} scales16")
     if group not in (64, 128):
         raise ValueError("group must be 64 or 128")
-    N = qweight.shape[0]
+    N = qweight.shape[0] if qweight.dim() == 2 else -1
     if qweight.dtype != torch.int32 or tuple(qweight.shape) != (N, K // 8):
         raise ValueError(f"{name} qweight must be int32 [N, K/8]")
     if scales16.dtype != torch.float16 or tuple(scales16.shape) != (N, K // group):
@@ -611,6 +611,12 @@ def _packed_check(x, K, qweight, scales16, zeros, group, name):
     _same_device(x, (qweight, f"{name} qweight"), (scales16, f"{name} scales16"),
                  (zeros, f"{name} zeros"))
     return N
+
+
+def _in_channels(qweight, name):
+    if qweight.dim() != 2:
+        raise ValueError(f"{name} must be int32 [N, K/8]")
+    return qweight.shape[1] * 8
 
 
 def _packed_arg(qweight, scales16, zeros):
@@ -660,8 +666,8 @@ def w4a16_gated(A: torch.Tensor, gate_qweight: torch.Tensor, gate_scales16: torc
     out = _out(out, (M, N), torch.float16, A.device)
     ws = _scratch(workspace, lib.w4a16_gated_workspace_bytes(M, N, K, 0), A.device)
     _launch("w4a16_gated", lib.w4a16_gated, A.device,
-        A.data_ptr(), M, N, K, group, _ACTS[act], _packed_arg(*gate), _packed_arg(*up),
-        out.data_ptr(), *_ws_args(ws))
+            A.data_ptr(), M, N, K, group, _ACTS[act], _packed_arg(*gate), _packed_arg(*up),
+            out.data_ptr(), *_ws_args(ws))
     return out
 
 
@@ -696,9 +702,9 @@ def w4a16_gated_ckpt(A: torch.Tensor, gate_qweight: torch.Tensor, gate_scales16:
               for _ in range(2))
     ws = _scratch(workspace, lib.w4a16_gated_workspace_bytes(M, N, K, 1), dev)
     _launch("w4a16_gated_ckpt", lib.w4a16_gated_ckpt, dev,
-        A.data_ptr(), M, N, K, group, _ACTS[act], _packed_arg(*gate), _packed_arg(*up),
-        H.data_ptr(), g8.data_ptr(), gs.data_ptr(), u8.data_ptr(), us.data_ptr(),
-        fl, *_ws_args(ws))
+            A.data_ptr(), M, N, K, group, _ACTS[act], _packed_arg(*gate), _packed_arg(*up),
+            H.data_ptr(), g8.data_ptr(), gs.data_ptr(), u8.data_ptr(), us.data_ptr(),
+            fl, *_ws_args(ws))
     return GatedResult(H, g8, gs, u8, us, flags)
 
 
@@ -723,7 +729,7 @@ def w4a16_gated_backward(dH: torch.Tensor, g8: torch.Tensor, g_scales: torch.Ten
         _fp8_check(q, s, 1, nm)
         if tuple(q.shape) != (M, N):
             raise ValueError(f"{nm} must have dH's shape")
-    K = gate_qweight.shape[1] * 8
+    K = _in_channels(gate_qweight, "gate qweight")
     gate = (gate_qweight, gate_scales16, gate_zeros)
     up = (up_qweight, up_scales16, up_zeros)
     if _gated_check(dH, K, gate, up, group, act) != N:
@@ -733,9 +739,9 @@ def w4a16_gated_backward(dH: torch.Tensor, g8: torch.Tensor, g_scales: torch.Ten
     ws = _scratch(workspace, lib.w4a16_gated_backward_workspace_bytes(
         M, N, K, group, int(gate_zeros is not None)), dH.device)
     _launch("w4a16_gated_backward", lib.w4a16_gated_backward, dH.device,
-        dH.data_ptr(), g8.data_ptr(), g_scales.data_ptr(), u8.data_ptr(), u_scales.data_ptr(),
-        M, N, K, group, _ACTS[act], _packed_arg(*gate), _packed_arg(*up), out.data_ptr(),
-        *_ws_args(ws))
+            dH.data_ptr(), g8.data_ptr(), g_scales.data_ptr(), u8.data_ptr(), u_scales.data_ptr(),
+            M, N, K, group, _ACTS[act], _packed_arg(*gate), _packed_arg(*up), out.data_ptr(),
+            *_ws_args(ws))
     return out
 
 
@@ -753,7 +759,7 @@ def w4a16_gemm_backward(dY: torch.Tensor, qweight: torch.Tensor, scales16: torch
     lib = _lib.load()
     _halves(dY, "dY")
     M, N = dY.shape
-    K = qweight.shape[1] * 8
+    K = _in_channels(qweight, "qweight")
     if _packed_check(dY, K, qweight, scales16, zeros, group, "the weight's") != N:
         raise ValueError("the weight's rows must be dY's columns")
     if s16 is not None:
@@ -765,7 +771,7 @@ def w4a16_gemm_backward(dY: torch.Tensor, qweight: torch.Tensor, scales16: torch
     ws = _scratch(workspace, lib.w4a16_gemm_backward_workspace_bytes(
         M, N, K, group, int(zeros is not None)), dY.device)
     _launch("w4a16_gemm_backward", lib.w4a16_gemm_backward, dY.device,
-        dY.data_ptr(), M, N, K, group, qweight.data_ptr(), scales16.data_ptr(),
-        zeros.data_ptr() if zeros is not None else None,
-        s16.data_ptr() if s16 is not None else None, out.data_ptr(), *_ws_args(ws))
+            dY.data_ptr(), M, N, K, group, qweight.data_ptr(), scales16.data_ptr(),
+            zeros.data_ptr() if zeros is not None else None,
+            s16.data_ptr() if s16 is not None else None, out.data_ptr(), *_ws_args(ws))
     return out

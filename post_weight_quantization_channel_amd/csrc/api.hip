@@ -581,17 +581,21 @@ awq_status w4a16_gemm_ws(const uint16_t* A, int64_t M, int64_t N, int64_t K, int
 namespace {
 
 // 8-bit operands: rows of K codes, K a multiple of 16, so that rows and 16-byte chunks stay
-// aligned; 256 rows of a tile must fit a 32-bit buffer range.
+// aligned; 256 rows of a tile must fit a 32-bit buffer range. A launch holds fewer than 2^32
+// threads: 16 per block of 128 values in the quantizer, 512 per row in the gradients' first pass.
 constexpr int64_t kMaxFp8K = int64_t(1) << 20;
+constexpr int64_t kMaxFp8Blocks = (int64_t(1) << 28) - 16;
+constexpr int64_t kMaxGradRows = int64_t(1) << 22;
+constexpr int64_t kMaxOutputs = int64_t(1) << 36;
 
 bool fp8_matrix_ok(int64_t M, int64_t K, int32_t block_rows) {
   return M >= 1 && K >= 16 && K % 16 == 0 && M <= kMaxDim && K <= kMaxDim &&
-         M * ((K + 127) / 128) <= (int64_t(1) << 31) && (block_rows == 1 || block_rows == 128);
+         M * ((K + 127) / 128) <= kMaxFp8Blocks && (block_rows == 1 || block_rows == 128);
 }
 
 awq_status check_fp8_gemm(int64_t M, int64_t N, int64_t K) {
   if (M < 1 || N < 1 || K < 16 || K % 16 || M > kMaxDim || N > kMaxDim || K > kMaxFp8K ||
-      M * N > (int64_t(1) << 38))
+      M * N > kMaxOutputs)
     return AWQ_ERR_SHAPE;
   return AWQ_OK;
 }
@@ -650,7 +654,7 @@ bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0
 // sizes of a product with packed weights [N, K] and M rows
 bool packed_sizes_ok(int64_t M, int64_t N, int64_t K) {
   return M >= 1 && N >= 1 && K >= 128 && K % 128 == 0 && M <= kMaxDim && N <= kMaxDim &&
-         K <= kMaxW4A16K && M * N <= (int64_t(1) << 38);
+         K <= kMaxW4A16K && M * N <= kMaxOutputs;
 }
 
 awq_status check_gated(int64_t M, int64_t N, int64_t K, int32_t group, int32_t act,
@@ -674,6 +678,11 @@ awq::GatedWeights gated_weights(const awq_packed* gate, const awq_packed* up) {
   return awq::GatedWeights{{gate->qweight, up->qweight},
                            {gate->scales16, up->scales16},
                            {gate->zeros, up->zeros}};
+}
+
+// sizes of a gradient with M rows
+bool grad_sizes_ok(int64_t M, int64_t N, int64_t K) {
+  return packed_sizes_ok(M, N, K) && M <= kMaxGradRows;
 }
 
 // N of the 8-bit activations: rows of whole 16-byte chunks
@@ -718,7 +727,7 @@ awq_status w4a16_gated_ckpt(const uint16_t* A, int64_t M, int64_t N, int64_t K, 
 
 size_t w4a16_gated_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t group,
                                             int32_t zero_point) {
-  if (!packed_sizes_ok(M, N, K) || !saved_sizes_ok(N) || (group != 128 && group != 64)) return 0;
+  if (!grad_sizes_ok(M, N, K) || !saved_sizes_ok(N) || (group != 128 && group != 64)) return 0;
   return awq::w4a16_grad_plan(M, N, K, group, true, zero_point != 0).ws_bytes;
 }
 
@@ -730,8 +739,8 @@ awq_status w4a16_gated_backward(const uint16_t* dH, const uint8_t* g8, const flo
   if (!dH || !g8 || !g_scales || !u8 || !u_scales || !dA) return AWQ_ERR_NULL;
   const awq_status cs = check_gated(M, N, K, group, act, gate, up);
   if (cs != AWQ_OK) return cs;
-  if (!saved_sizes_ok(N) || !aligned16(dH) || !aligned16(g8) || !aligned16(u8) || !aligned16(dA) ||
-      !aligned4(g_scales) || !aligned4(u_scales))
+  if (!grad_sizes_ok(M, N, K) || !saved_sizes_ok(N) || !aligned16(dH) || !aligned16(g8) ||
+      !aligned16(u8) || !aligned16(dA) || !aligned4(g_scales) || !aligned4(u_scales))
     return AWQ_ERR_SHAPE;
   const size_t need =
       awq::w4a16_grad_plan(M, N, K, group, true, gate->zeros != nullptr).ws_bytes;
@@ -743,7 +752,7 @@ awq_status w4a16_gated_backward(const uint16_t* dH, const uint8_t* g8, const flo
 
 size_t w4a16_gemm_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t group,
                                            int32_t zero_point) {
-  if (!packed_sizes_ok(M, N, K) || (group != 128 && group != 64)) return 0;
+  if (!grad_sizes_ok(M, N, K) || (group != 128 && group != 64)) return 0;
   return awq::w4a16_grad_plan(M, N, K, group, false, zero_point != 0).ws_bytes;
 }
 
@@ -753,7 +762,7 @@ awq_status w4a16_gemm_backward(const uint16_t* dY, int64_t M, int64_t N, int64_t
                                size_t ws_bytes, hipStream_t stream) {
   if (!dY || !qweight || !scales16 || !dA) return AWQ_ERR_NULL;
   if (group != 128 && group != 64) return AWQ_ERR_CONFIG;
-  if (!packed_sizes_ok(M, N, K) || !aligned2(dY) || !aligned16(qweight) || !aligned2(scales16) ||
+  if (!grad_sizes_ok(M, N, K) || !aligned2(dY) || !aligned16(qweight) || !aligned2(scales16) ||
       !aligned16(dA) || (s16 && !aligned2(s16)))
     return AWQ_ERR_SHAPE;
   const size_t need = awq::w4a16_grad_plan(M, N, K, group, false, zeros != nullptr).ws_bytes;

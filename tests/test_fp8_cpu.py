@@ -31,8 +31,11 @@ def test_quantize_refuses(lib):
         (1, -1, DTYPE), (2, 0, SHAPE), (2, -1, SHAPE), (2, (1 << 24) + 1, SHAPE), (3, 0, SHAPE),
         (3, 8, SHAPE), (3, 250, SHAPE), (4, 248, SHAPE), (4, 257, SHAPE), (5, 0, CONFIG),
         (5, 64, CONFIG), (0, P + 8, SHAPE), (6, P + 4, SHAPE), (7, P + 2, SHAPE)])
-    big = [P, 1, 1 << 24, 1 << 16, 1 << 16, 1, P, P, P, None]      # more than 2^31 blocks
+    big = [P, 1, 1 << 24, 1 << 16, 1 << 16, 1, P, P, P, None]      # more than 2^28 blocks
     assert lib.awq_fp8_quantize(*big) == SHAPE
+    big[2] = (1 << 19) + 1
+    assert lib.awq_fp8_quantize(*big) == SHAPE
+    assert lib.awq_fp8_dequantize(P, P, (1 << 19) + 1, 1 << 16, 1, 1, P, None) == SHAPE
 
 
 def test_dequantize_refuses(lib):
@@ -49,6 +52,7 @@ def test_gemm_refuses(lib):
         (7, 0, DTYPE), (7, 5, DTYPE), (4, 0, SHAPE), (5, 0, SHAPE), (6, 0, SHAPE), (6, 40, SHAPE),
         (6, (1 << 20) + 16, SHAPE), (4, (1 << 24) + 1, SHAPE), (0, P + 8, SHAPE),
         (2, P + 4, SHAPE), (8, P + 2, SHAPE), (1, P + 1, SHAPE), (3, P + 2, SHAPE)])
+    assert lib.awq_fp8_gemm(P, P, P, P, 1 << 19, (1 << 17) + 1, 256, 1, P, None, 0, None) == SHAPE
     need = lib.awq_fp8_gemm_workspace_bytes(100, 256, 4096)
     assert need > 0
     split = [P, P, P, P, 100, 256, 4096, 1, P, P, need - 1, None]

@@ -85,6 +85,10 @@ def test_gated_backward_refuses(lib):
              (0, P + 2, SHAPE), (1, P + 8, SHAPE), (3, P + 1, SHAPE), (2, P + 2, SHAPE),
              (12, P + 8, SHAPE), (8, 96, CONFIG), (9, 2, CONFIG)] + sizes(5, 6, 7) +
             [(10, w, s) for w, s in WEIGHTS])
+    rows = (1 << 22) + 1
+    assert lib.w4a16_gated_backward_workspace_bytes(rows, 16, 128, 128, 0) == 0
+    assert lib.w4a16_gated_backward(P, P, P, P, P, rows, 16, 128, 128, 0, pk(), pk(), P, P, BIG,
+                                    None) == SHAPE
     need = lib.w4a16_gated_backward_workspace_bytes(4, 64, 256, 128, 0)
     good[14] = need - 1
     assert need > 0 and lib.w4a16_gated_backward(*good) == WORKSPACE
@@ -100,6 +104,10 @@ def test_gemm_backward_refuses(lib):
              (5, P + 8, SHAPE), (6, P + 1, SHAPE), (8, P + 1, SHAPE), (9, P + 8, SHAPE),
              (4, 0, CONFIG)] + sizes(1, 2, 3))
     assert lib.w4a16_gemm_backward_workspace_bytes(4, 64, 250, 128, 0) == 0
+    rows = (1 << 22) + 1
+    assert lib.w4a16_gemm_backward_workspace_bytes(rows, 16, 128, 128, 0) == 0
+    assert lib.w4a16_gemm_backward(P, rows, 16, 128, 128, P, P, None, P, P, P, BIG, None) == SHAPE
+    assert lib.w4a16_gated(P, 1 << 19, (1 << 17) + 1, 128, 128, 0, pk(), pk(), P, P, BIG, None) == SHAPE
 
 
 def test_binding_refuses_before_the_call():
