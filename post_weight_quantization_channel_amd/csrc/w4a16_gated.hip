@@ -680,9 +680,12 @@ GatedPlan w4a16_gated_plan(int64_t M, int64_t N, int64_t K, bool ckpt) {
   GatedPlan p{};
   p.S = 1;
   if (!ckpt && M <= 32) return p;
-  p.bm = M > 64 ? 128 : 64;
-  p.tm = (M + p.bm - 1) / p.bm;
   p.tn = (N + kTN - 1) / kTN;
+  // 128 rows share a decoded weight tile (64 against 128 rows, us: 512 x 11008 x 4096 114 and 112,
+  // groups of 64 with zero points 210 and 148); with 16 such tiles or fewer the finer split of
+  // rows fills more CUs (256 x 1024 x 4096: 23 and 26, groups of 64 27 and 30)
+  p.bm = M > 64 && (M + 127) / 128 * p.tn > 16 ? 128 : 64;
+  p.tm = (M + p.bm - 1) / p.bm;
   p.Np = p.tn * kTN;
   const int64_t KB = K / 128, tiles = p.tm * p.tn;
   if (tiles < 256) {   // two workgroups per CU, at least 4 steps each
