@@ -431,6 +431,7 @@ awq_status awq_act_stats_noalloc(const void* X, awq_dtype xdt, int64_t M, int64_
  *          in bf16 and fp32.
  * flags    in/out, or NULL: NONFINITE_X (an Inf or NaN, whose code is NaN; the block's scale is
  *          that of its finite values).
+ * Outputs and workspaces of this call and of those below share no memory with an input.
  * Errors: AWQ_ERR_NULL, AWQ_ERR_DTYPE, AWQ_ERR_CONFIG (block_rows), AWQ_ERR_SHAPE (sizes, ldx,
  *         misalignment; more than 2^28 - 16 blocks of 1 x 128).
  * ---------------------------------------------------------------------------------------- */

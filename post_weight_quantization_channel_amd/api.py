@@ -485,12 +485,22 @@ def _launch(call: str, fn, device: torch.device, *args) -> None:
         check(call, status)
 
 
-def _out(out, shape, dtype, device) -> torch.Tensor:
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two contiguous tensors share memory."""
+    pa, pb = a.data_ptr(), b.data_ptr()
+    return pa < pb + b.numel() * b.element_size() and pb < pa + a.numel() * a.element_size()
+
+
+def _out(out, shape, dtype, device, *inputs) -> torch.Tensor:
+    """The caller's output (checked), or a new one. Workgroups read the inputs while others write,
+    so the output must be apart from them."""
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
     _dev(out, "out")
     if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device:
         raise ValueError(f"out must be {dtype} {tuple(shape)} on {device}")
+    if any(t is not None and _overlap(out, t) for t in inputs):
+        raise ValueError("out must not share memory with an input")
     return out
 
 
@@ -556,7 +566,7 @@ def fp8_dequantize(q: torch.Tensor, scales: torch.Tensor, block_rows: int = 1,
         raise ValueError("dtype must be fp16, bf16 or fp32")
     _same_device(q, (scales, "scales"))
     M, K = q.shape
-    out = _out(out, (M, K), dtype, q.device)
+    out = _out(out, (M, K), dtype, q.device, q, scales)
     _launch("awq_fp8_dequantize", lib.awq_fp8_dequantize, q.device,
             q.data_ptr(), scales.data_ptr(), M, K, block_rows, _DT[dtype], out.data_ptr())
     return out
@@ -581,7 +591,7 @@ def fp8_gemm(A8: torch.Tensor, a_scales: torch.Tensor, W8: torch.Tensor, w_scale
         raise ValueError("out_dtype must be fp16 or bf16")
     dev = A8.device
     _same_device(A8, (a_scales, "a_scales"), (W8, "W8"), (w_scales, "w_scales"))
-    out = _out(out, (M, N), out_dtype, dev)
+    out = _out(out, (M, N), out_dtype, dev, A8, a_scales, W8, w_scales)
     ws = _scratch(workspace, lib.awq_fp8_gemm_workspace_bytes(M, N, K), dev)
     _launch("awq_fp8_gemm", lib.awq_fp8_gemm, dev,
             A8.data_ptr(), a_scales.data_ptr(), W8.data_ptr(), w_scales.data_ptr(), M, N, K,
@@ -663,7 +673,7 @@ def w4a16_gated(A: torch.Tensor, gate_qweight: torch.Tensor, gate_scales16: torc
     gate = (gate_qweight, gate_scales16, gate_zeros)
     up = (up_qweight, up_scales16, up_zeros)
     N = _gated_check(A, K, gate, up, group, act)
-    out = _out(out, (M, N), torch.float16, A.device)
+    out = _out(out, (M, N), torch.float16, A.device, A, *gate, *up)
     ws = _scratch(workspace, lib.w4a16_gated_workspace_bytes(M, N, K, 0), A.device)
     _launch("w4a16_gated", lib.w4a16_gated, A.device,
             A.data_ptr(), M, N, K, group, _ACTS[act], _packed_arg(*gate), _packed_arg(*up),
@@ -735,7 +745,7 @@ def w4a16_gated_backward(dH: torch.Tensor, g8: torch.Tensor, g_scales: torch.Ten
     if _gated_check(dH, K, gate, up, group, act) != N:
         raise ValueError("the weights' rows must be dH's columns")
     _same_device(dH, (g8, "g8"), (g_scales, "g_scales"), (u8, "u8"), (u_scales, "u_scales"))
-    out = _out(out, (M, K), torch.float16, dH.device)
+    out = _out(out, (M, K), torch.float16, dH.device, dH, g8, g_scales, u8, u_scales, *gate, *up)
     ws = _scratch(workspace, lib.w4a16_gated_backward_workspace_bytes(
         M, N, K, group, int(gate_zeros is not None)), dH.device)
     _launch("w4a16_gated_backward", lib.w4a16_gated_backward, dH.device,
@@ -767,7 +777,7 @@ def w4a16_gemm_backward(dY: torch.Tensor, qweight: torch.Tensor, scales16: torch
         if s16.dtype != torch.float16 or tuple(s16.shape) != (K,):
             raise ValueError("s16 must be fp16 [K]")
         _same_device(dY, (s16, "s16"))
-    out = _out(out, (M, K), torch.float16, dY.device)
+    out = _out(out, (M, K), torch.float16, dY.device, dY, qweight, scales16, zeros, s16)
     ws = _scratch(workspace, lib.w4a16_gemm_backward_workspace_bytes(
         M, N, K, group, int(zeros is not None)), dY.device)
     _launch("w4a16_gemm_backward", lib.w4a16_gemm_backward, dY.device,

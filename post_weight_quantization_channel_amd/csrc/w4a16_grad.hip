@@ -266,7 +266,7 @@ __global__ __launch_bounds__(512) void grad_rows_kernel(
 // spreads a wave's writes over all banks.
 // Step t computes from one stage while the values of step t + 1, loaded during step t - 1, are
 // folded and decoded into the other; one barrier per step.
-// Rows past M read row M - 1 and columns past K the last word; neither is stored.
+// Rows past M read as zeros and columns past K as the last word; neither is stored.
 template <int G, bool ZP, bool LO, int BM>
 __global__ __launch_bounds__(BM == 256 ? 512 : 256) void grad_gemm_kernel(
     GatedWeights W, GradShape S, const uint16_t* __restrict__ hi, const uint16_t* __restrict__ lo,

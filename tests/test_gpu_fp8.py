@@ -273,3 +273,13 @@ def test_fp8_gemm_streams_and_graph(awq, m):
         e1 = pair()
         torch.cuda.synchronize()
         assert torch.equal(y, e1) and torch.equal(e1, e2), i
+
+
+def test_output_apart_from_inputs(awq):
+    """An output in the memory of an operand is refused."""
+    a, w = awq.fp8_quantize(torch.randn(4, 256, device="cuda")), \
+        awq.fp8_quantize(torch.randn(128, 256, device="cuda"), block_rows=128)
+    with pytest.raises(ValueError, match="share memory"):
+        awq.fp8_gemm(a.q, a.scales, w.q, w.scales, out=a.q.view(torch.float16))
+    with pytest.raises(ValueError, match="share memory"):
+        awq.fp8_gemm(a.q, a.scales, w.q, w.scales, out=w.q[:4].view(torch.float16))

@@ -338,3 +338,25 @@ def test_outputs_end_where_they_should(awq, m):
     assert bool((buf[m:] == 5).all())
     assert bool((ws[need:] == 255).all())
     assert torch.equal(d, awq.w4a16_gated_backward(*args, group=64, **z))
+
+
+def test_output_apart_from_inputs(awq):
+    """An output that shares memory with an input, whole or in part, is refused; one that starts
+    where the input ends is not."""
+    n = k = 256
+    gate, up = packed(n, k, 128, False, 1), packed(n, k, 128, False, 2)
+    w, _ = on_gpu(gate, up)
+    buf = torch.randn(12, k, generator=torch.Generator().manual_seed(3)).half().cuda()
+    x = buf[4:8]
+    r = awq.w4a16_gated_ckpt(x, *w)
+    saved8 = (r.g8, r.g_scales, r.u8, r.u_scales)
+    for out in (buf[4:8], buf[3:7], buf[7:11]):
+        with pytest.raises(ValueError, match="share memory"):
+            awq.w4a16_gated(x, *w, out=out)
+        with pytest.raises(ValueError, match="share memory"):
+            awq.w4a16_gemm_backward(x, w[0], w[1], None, out=out)
+        with pytest.raises(ValueError, match="share memory"):
+            awq.w4a16_gated_backward(x, *saved8, *w, out=out)
+    want = awq.w4a16_gated(x, *w)
+    for out in (buf[:4], buf[8:]):
+        assert torch.equal(awq.w4a16_gated(x, *w, out=out), want)
