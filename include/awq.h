@@ -455,7 +455,7 @@ awq_status awq_fp8_dequantize(const uint8_t* q, const float* scales, int64_t M, 
  *          scales may be any fp32 numbers. Codes 16-byte aligned.
  * Y        out, [M, N] in ydt (AWQ_F16 or AWQ_BF16), 16-byte aligned; fp32 sums, rounded once.
  * ws       device workspace, 16-byte aligned, of at least awq_fp8_gemm_workspace_bytes(M, N, K)
- *          bytes (0: ws may be NULL): scratch for the partial sums of K slices (M > 64 while the
+ *          bytes (0: ws may be NULL): scratch for the partial sums of K slices (M > 8 while the
  *          output tiles number fewer than the CUs), which are added in a fixed order. Calls that
  *          share a workspace must not overlap.
  * Errors: AWQ_ERR_NULL, AWQ_ERR_DTYPE, AWQ_ERR_SHAPE (M < 1, N < 1, K < 16, K % 16, K > 2^20,
@@ -480,7 +480,7 @@ awq_status awq_fp8_gemm(const uint8_t* A8, const float* a_scales, const uint8_t*
  *          0.044715 g^3))).
  * ws       device workspace, 16-byte aligned, of at least w4a16_gated_workspace_bytes(M, N, K, 0)
  *          bytes (0: ws may be NULL): fp32 partials of g and u when K is split over workgroups
- *          (M > 32 while the tiles leave CUs idle), added in a fixed order. Calls that share a
+ *          (M > 16 while the tiles leave CUs idle), added in a fixed order. Calls that share a
  *          workspace must not overlap.
  * Errors: AWQ_ERR_NULL, AWQ_ERR_CONFIG (group, act, zeros on one side only), AWQ_ERR_SHAPE (M < 1,
  *         N < 1, K % 128, K > 32768, M N > 2^36, misalignment), AWQ_ERR_WORKSPACE.

@@ -9,9 +9,9 @@
 // channel sits at which of the 32 bytes a lane supplies does not matter as long as both operands
 // agree; lane group lg (lane / 16) supplies the 16-byte chunks lg and lg + 4 of a block.
 //
-//   M <= 64   fp8_skinny_kernel: bound by the weight's bytes, which go from memory straight into
+//   few rows  fp8_skinny_kernel (up to 8, or 48 on small weights): bound by the weight's bytes, which go from memory straight into
 //             the MFMA's registers; 8 waves of a workgroup share 16 weight rows and split K.
-//   M > 64    fp8_tiled_kernel: both operands through LDS, moved there by the buffer unit; with
+//   else      fp8_tiled_kernel: tiles of 64, 128 or 256 rows, both operands through LDS, moved there by the buffer unit; with
 //             fewer tiles than CUs K is split over workgroups and the fp32 partials are added in
 //             slice order by fp8_sum_slices_kernel.
 // Rounding: the instruction adds the channels in groups of 8 (of a lane's consecutive bytes), each
@@ -365,18 +365,29 @@ __global__ __launch_bounds__(256) void fp8_sum_slices_kernel(const float* __rest
   }
 }
 
+// Which kernel. A workgroup of the skinny kernel reads all activations for 16 weight rows, which
+// costs more than the weight's bytes as M grows; the tiled one with K slices is two launches, a few
+// us, which small weights do not earn back. Skinny and tiled, us:
+//   28672 x 8192: M = 8 57 and 57, M = 16 70 and 58, M = 64 178 and 66
+//   11008 x 4096: M = 8 14.5 and 14.5, M = 16 17.7 and 15.1, M = 64 41 and 21
+//   4096 x 4096:  M = 16 9.3 and 13.8, M = 48 13.7 and 13.9, M = 64 15.5 and 13.8
+static bool skinny(int64_t M, int64_t N, int64_t K) {
+  return M <= 8 || (M <= 48 && N * K <= (int64_t(1) << 24));
+}
+
 Fp8GemmPlan fp8_gemm_plan(int64_t M, int64_t N, int64_t K) {
   Fp8GemmPlan p{};
   const int64_t KB = (K + 127) / 128;
   p.S = 1;
   p.steps = KB;
-  if (M <= 64) return p;
+  if (skinny(M, N, K)) return p;
   const int64_t t256 = ((M + 255) / 256) * ((N + 255) / 256);
   // 256-row tiles while they fill the CUs and are not half empty (128 rows instead, us:
   // 100 x 65536 x 4096 79 to 74, 77 x 80000 x 2048 62 to 49)
-  p.tile = t256 >= 256 && M > 128 ? 256 : 128;
-  const int64_t tiles = ((M + p.tile - 1) / p.tile) * ((N + p.tile - 1) / p.tile);
-  if (p.tile == 128 && tiles < 256) {
+  p.tile = t256 >= 256 && M > 128 ? 256 : M > 64 ? 128 : 64;
+  const int64_t bn = p.tile == 256 ? 256 : 128;
+  const int64_t tiles = ((M + p.tile - 1) / p.tile) * ((N + bn - 1) / bn);
+  if (p.tile != 256 && tiles < 256) {
     int64_t S = 512 / tiles;
     const int64_t smax = KB / 4;
     S = S > smax ? smax : S;
@@ -393,7 +404,7 @@ template <int DT>
 static hipError_t fp8_gemm_dt(const uint8_t* A, const float* sa, const uint8_t* W, const float* sw,
                               int64_t M, int64_t N, int64_t K, uint16_t* Y, void* ws,
                               hipStream_t stream) {
-  if (M <= 64) {
+  if (skinny(M, N, K)) {
     const unsigned grid = (unsigned)((N + 15) / 16);
 #define AWQ_SK(MT_, U_)                                                                \
   fp8_skinny_kernel<MT_, U_, DT><<<grid, 64 * kSkWaves, 0, stream>>>(A, sa, W, sw, M, N, K, Y)
@@ -403,14 +414,17 @@ static hipError_t fp8_gemm_dt(const uint8_t* A, const float* sa, const uint8_t* 
   }
   const Fp8GemmPlan p = fp8_gemm_plan(M, N, K);
   const uint32_t tm = (uint32_t)((M + p.tile - 1) / p.tile);
-  const uint32_t tn = (uint32_t)((N + p.tile - 1) / p.tile);
+  const int64_t bn = p.tile == 256 ? 256 : 128;
+  const uint32_t tn = (uint32_t)((N + bn - 1) / bn);
   const uint32_t tiles = tm * tn;
   float* P = p.S > 1 ? static_cast<float*>(ws) : nullptr;
 #define AWQ_FT(BM_, BN_, WM_, WN_)                                                             \
   fp8_tiled_kernel<BM_, BN_, WM_, WN_, DT><<<tiles * (unsigned)p.S, 64 * WM_ * WN_,            \
                                              2 * ((BM_ + BN_) * 128 + 4 * BM_), stream>>>(     \
       A, sa, W, sw, M, N, K, Y, tm, tn, (int)p.steps, P, p.stride)
-  if (p.tile == 256) AWQ_FT(256, 256, 2, 4); else AWQ_FT(128, 128, 2, 2);
+  if (p.tile == 256) AWQ_FT(256, 256, 2, 4);
+  else if (p.tile == 128) AWQ_FT(128, 128, 2, 2);
+  else AWQ_FT(64, 128, 1, 4);
 #undef AWQ_FT
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.S == 1) return e;

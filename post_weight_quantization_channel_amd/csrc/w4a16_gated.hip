@@ -9,7 +9,7 @@
 // fp32 until H is rounded once, and until they are cut to 8 bits.
 //   M <= 2    w4a16_gated_gemv_kernel: bound by the codes' bytes; a wave owns one output channel,
 //             its gate row and its up row.
-//   M <= 32   w4a16_gated_skinny_kernel: MFMA, codes from memory to registers, K over 8 waves.
+//   few rows  w4a16_gated_skinny_kernel (up to 16, or 32 on small weights): MFMA, codes from memory to registers, K over 8 waves.
 //   else      w4a16_gated_tiled_kernel: 128 (or 64) rows x 128 output channels; with few tiles K is
 //             split over workgroups and w4a16_gated_finish_kernel adds the slices in order and applies
 //             the activation. The 8-bit form always takes this path: 128 output channels of a
@@ -676,10 +676,20 @@ __global__ __launch_bounds__(256) void w4a16_gated_finish_kernel(
 
 // ---- plans and launches ---------------------------------------------------------------------
 
+// Which kernel. The skinny one decodes 16 output channels' codes once for up to 32 rows but reads the
+// activations once per 16 channels; the tiled one with K slices is two launches. Skinny and
+// tiled, us (groups of 128):
+//   28672 x 8192: M = 16 105 and 103, M = 17 124 and 103, M = 32 160 and 106
+//   11008 x 4096: M = 16 24.4 and 28.3, M = 17 30.7 and 28.4, M = 32 37.7 and 30.0
+//   4096 x 4096:  M = 16 11.3 and 16.2, M = 32 13.5 and 18.2
+static bool skinny(int64_t M, int64_t N, int64_t K) {
+  return M <= 16 || (M <= 32 && N * K <= (int64_t(1) << 24));
+}
+
 GatedPlan w4a16_gated_plan(int64_t M, int64_t N, int64_t K, bool ckpt) {
   GatedPlan p{};
   p.S = 1;
-  if (!ckpt && M <= 32) return p;
+  if (!ckpt && skinny(M, N, K)) return p;
   p.tn = (N + kTN - 1) / kTN;
   // 128 rows share a decoded weight tile (64 against 128 rows, us: 512 x 11008 x 4096 114 and 112,
   // groups of 64 with zero points 210 and 148); with 16 such tiles or fewer the finer split of
@@ -722,7 +732,7 @@ static hipError_t gated(const uint16_t* A, int64_t M, int64_t N, int64_t K, cons
 #undef AWQ_GG
     return hipGetLastError();
   }
-  if (!ckpt && M <= 32) {
+  if (!ckpt && skinny(M, N, K)) {
     const unsigned grid = (unsigned)((N + 15) / 16);
     const int mt = M <= 16 ? 1 : 2;
     const size_t lds = (size_t)kSkWaves * 2 * mt * 64 * sizeof(floatx4);

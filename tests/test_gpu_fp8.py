@@ -197,7 +197,8 @@ def _dev(codes):
 # one row to two tiles; N and K off every tile; one and several K slices; the 256-row tile
 GEMM = [(1, 16, 16), (1, 1, 128), (2, 130, 144), (16, 128, 256), (17, 33, 1040), (33, 100, 2064),
         (64, 257, 4112), (65, 130, 144), (100, 1000, 4112), (128, 128, 128), (129, 385, 1168),
-        (200, 64, 8192), (300, 260, 16), (1, 4096, 4096), (4097, 4100, 144)]
+        (200, 64, 8192), (300, 260, 16), (1, 4096, 4096), (4097, 4100, 144),
+        (8, 4112, 4112), (9, 4112, 4112), (50, 4111, 4112), (49, 130, 144), (64, 128, 1040)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])

@@ -56,7 +56,8 @@ def check(y, want, slack, dtype=torch.float16):
 # one row; two; the MFMA paths at their edges; tiles; odd N; one and several K slices
 FORWARD = [(1, 1, 128), (1, 130, 4224), (1, 64, 8320), (2, 257, 1024), (2, 40, 8192), (3, 16, 128),
            (16, 100, 1152), (17, 31, 2048), (32, 128, 640), (33, 1, 128), (64, 250, 4096),
-           (65, 129, 1024), (128, 384, 256), (300, 200, 512), (300, 1100, 2048), (700, 4112, 128)]
+           (65, 129, 1024), (128, 384, 256), (300, 200, 512), (300, 1100, 2048), (700, 4112, 128),
+           (17, 4200, 4096), (32, 4104, 4224)]
 
 
 @pytest.mark.parametrize("group,zp,act", [(128, False, "silu"), (64, True, "gelu"),
