@@ -379,7 +379,8 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
   uint32_t voff[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)   // load j of wave w: rows TM / 4 w + 4 j + lane / 16
-    voff[j] = (uint32_t)(lg * K * 2) + (uint32_t)((li ^ (4 * j + lg)) << 4);
+    voff[j] = (uint32_t)(lg * K * 2) +
+              (uint32_t)((li ^ (4 * ((TM / 16 * wave + j) & 3) + lg)) << 4);
   auto issue = [&](int b, int st) {
 #pragma unroll
     for (int j = 0; j < MB; ++j) {
@@ -401,26 +402,58 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
     if (ZP) rz[r] = make_rsrc(W.z[r] + n0 * (K / GS), nrows * (uint32_t)(K / GS));
     const uint32_t row = (uint32_t)(32 * wave + 16 * r + li);
     qoff[r] = row * (uint32_t)(K / 2) + (uint32_t)lg * (GS == 128 ? 16u : 8u);
-    goff[r] = row * (uint32_t)(K / GS);
+    goff[r] = (row * (uint32_t)(K / GS) + (uint32_t)(lg * kG));
   }
   struct Codes {
-    uint32_t w[4][4], st[4], z[4];   // st, z: groups of 64 hold both groups' values
+    uint32_t w[4][4];
   };
   auto load_codes = [&](int b, Codes& c) {
-    const uint32_t qs = (uint32_t)b * 64u, gs = (uint32_t)b * (uint32_t)kG;
+    const uint32_t qs = (uint32_t)b * 64u;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int r = t >> 1, h = t & 1;
       if (GS == 128) {
         const uint4 v = buffer_load16(rq[r], qoff[h], qs);
         c.w[t][0] = v.x; c.w[t][1] = v.y; c.w[t][2] = v.z; c.w[t][3] = v.w;
-        c.st[t] = buffer_load2(rst[r], 2u * goff[h], 2u * gs);
-        if (ZP) c.z[t] = buffer_load1(rz[r], goff[h], gs);
       } else {
         const uint2 v = buffer_load8(rq[r], qoff[h], qs), x = buffer_load8(rq[r], qoff[h] + 32u, qs);
         c.w[t][0] = v.x; c.w[t][1] = v.y; c.w[t][2] = x.x; c.w[t][3] = x.y;
-        c.st[t] = buffer_load4(rst[r], 2u * goff[h], 2u * gs);
-        if (ZP) c.z[t] = buffer_load2(rz[r], goff[h], gs);
+      }
+    }
+  };
+  // Group steps and zero points of four K steps at a time, K step b + lg in lane group lg (every lane
+  // loading the step that it uses was four times the loads, of two bytes a row each, and they bound
+  // the kernel); spread(j) hands those of the j-th K step to all lane groups.
+  struct Steps {
+    uint32_t st[4], z[4];   // groups of 64: both groups' values
+  };
+  Steps sv;
+  auto load_steps = [&](int b) {
+    const uint32_t gs = (uint32_t)b * (uint32_t)kG;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int r = t >> 1, h = t & 1;
+      if (GS == 128) {
+        sv.st[t] = buffer_load2(rst[r], 2u * goff[h], 2u * gs);
+        if (ZP) sv.z[t] = buffer_load1(rz[r], goff[h], gs);
+      } else {
+        sv.st[t] = buffer_load4(rst[r], 2u * goff[h], 2u * gs);
+        if (ZP) sv.z[t] = buffer_load2(rz[r], goff[h], gs);
+      }
+    }
+  };
+  auto spread = [&](int j, Steps& c) {
+    const int from = 4 * (16 * j + li);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if (GS == 128) {   // one word: the step below the zero point
+        const uint32_t v = (uint32_t)__builtin_amdgcn_ds_bpermute(
+            from, (int)(ZP ? sv.st[t] | sv.z[t] << 16 : sv.st[t]));
+        c.st[t] = ZP ? v & 0xFFFFu : v;
+        if (ZP) c.z[t] = v >> 16;
+      } else {
+        c.st[t] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)sv.st[t]);
+        if (ZP) c.z[t] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)sv.z[t]);
       }
     }
   };
@@ -436,7 +469,7 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
   // block ahead, among the matrix instructions of the block before (512 rows of 11008 x 4096 with zero
   // points: 167 us, 203 without); groups of 128 have no registers left for that (1100 us instead
   // of 830 for 4096 rows), and half as much scaling per instruction.
-  auto compute = [&](int st, const Codes& c) {
+  auto compute = [&](int st, const Codes& c, const Steps& g) {
     const char* sa = smem + st * kStage;
     constexpr int kK = 4 / kG;
     constexpr bool kAhead = GS == 64;
@@ -446,8 +479,8 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
       bool none[4];   // a step of 0: the codes are taken as ones that decode to 0
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const float s = h2f((uint16_t)(h == 0 ? c.st[t] & 0xFFFFu : c.st[t] >> 16));
-        const float z = ZP ? (float)(GS == 128 ? c.z[t] : h == 0 ? c.z[t] & 0xFFu : c.z[t] >> 8) : 8.0f;
+        const float s = h2f((uint16_t)(h == 0 ? g.st[t] & 0xFFFFu : g.st[t] >> 16));
+        const float z = ZP ? (float)(GS == 128 ? g.z[t] : h == 0 ? g.z[t] & 0xFFu : g.z[t] >> 8) : 8.0f;
         none[t] = s == 0.0f;
         nsub[t] = decode_nsub(ZP && none[t] ? 0.0f : z);
         const float now = none[t] ? prev[t] : s;
@@ -501,14 +534,19 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
   Codes cb[2];
   issue(b0, 0);
   load_codes(b0, cb[0]);
+  load_steps(b0);
   auto step = [&](int b, int st, const Codes& cur, Codes& nxt) {
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
     __syncthreads();
+    const int j = (b - b0) & 3;
+    Steps g;
+    spread(j, g);
     if (b + 1 < b1) {
       issue(b + 1, st ^ 1);
       load_codes(b + 1, nxt);
+      if (j == 3) load_steps(b + 1);
     }
-    compute(st, cur);
+    compute(st, cur, g);
   };
   for (int b = b0; b < b1; b += 2) {
     step(b, 0, cb[0], cb[1]);
@@ -698,12 +736,12 @@ GatedPlan w4a16_gated_plan(int64_t M, int64_t N, int64_t K, bool ckpt) {
   // 128 rows share a decoded weight tile (64 against 128 rows, us: 512 x 11008 x 4096 114 and 112,
   // groups of 64 with zero points 210 and 148); with 16 such tiles or fewer the finer split of
   // rows fills more CUs (256 x 1024 x 4096: 23 and 26, groups of 64 27 and 30)
-  p.bm = M > 64 && (M + 127) / 128 * p.tn > 16 ? 128 : 64;
+  p.bm = M > 64 && (M + 127) / 128 * p.tn > 16 ? 128 : M > 32 ? 64 : 32;
   p.tm = (M + p.bm - 1) / p.bm;
   p.Np = p.tn * kTN;
   const int64_t KB = K / 128, tiles = p.tm * p.tn;
   if (tiles < 256) {   // two workgroups per CU, at least 4 steps each
-    p.S = 512 / tiles;
+    p.S = (p.bm == 32 ? 1024 : 512) / tiles;
     const int64_t smax = KB / 4;
     p.S = p.S > smax ? smax : p.S;
     p.S = p.S < 1 ? 1 : p.S;
@@ -756,8 +794,10 @@ static hipError_t gated(const uint16_t* A, int64_t M, int64_t N, int64_t K, cons
       A, M, N, K, W, O, (uint32_t)p.tm, (uint32_t)p.tn, (int)p.steps, P, p.Np)
   if (p.bm == 128) {
     if (ckpt) AWQ_GT(true, 128); else AWQ_GT(false, 128);
-  } else {
+  } else if (p.bm == 64) {
     if (ckpt) AWQ_GT(true, 64); else AWQ_GT(false, 64);
+  } else {
+    if (ckpt) AWQ_GT(true, 32); else AWQ_GT(false, 32);
   }
 #undef AWQ_GT
   const hipError_t e = hipGetLastError();
