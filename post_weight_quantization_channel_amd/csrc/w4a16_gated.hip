@@ -10,12 +10,12 @@
 //   M <= 2    w4a16_gated_gemv_kernel: bound by the codes' bytes; a wave owns one output channel,
 //             its gate row and its up row.
 //   few rows  w4a16_gated_skinny_kernel (up to 16, or 32 on small weights): MFMA, codes from memory to registers, K over 8 waves.
-//   else      w4a16_gated_tiled_kernel: 128 (or 64) rows x 128 output channels; with few tiles K is
+//   else      w4a16_gated_tiled_kernel: 128 (64, 32) rows x 128 output channels; with few tiles K is
 //             split over workgroups and w4a16_gated_finish_kernel adds the slices in order and applies
 //             the activation. The 8-bit form always takes this path: 128 output channels of a
 //             tile are one block of the format.
-// Measured per call: 1 row of 11008 x 4096 11.6 us (46.5 MB, 4.0 TB/s); 16 rows 24 us; 512 rows,
-// groups of 64 with zero points, 148 us (0.62 PFLOP/s); 4096 rows with the 8-bit form 782 us (0.94
+// Measured per call: 1 row of 11008 x 4096 11.6 us (46.5 MB, 4.0 TB/s); 16 rows 21.5 us; 512 rows,
+// groups of 64 with zero points, 148 us (0.62 PFLOP/s); 4096 rows with the 8-bit form 760 us (0.97
 // PFLOP/s; matrix units busy 44% of the cycles at 1.96 GHz, the decode's and scaling's vector
 // instructions 42%).
 #include "fp8_format.h"
@@ -257,19 +257,13 @@ __global__ __launch_bounds__(64 * kSkWaves) void w4a16_gated_skinny_kernel(
     for (int t = 0; t < MT; ++t) acc[r][t] = floatx4{0.f, 0.f, 0.f, 0.f};
 
   struct Block {
-    uint32_t w[2][4], st[2][kG], z[2][kG];
+    uint32_t w[2][4];
     half8_t a[MT][4];
   };
   auto load = [&](int kb, Block& b) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       load_block<GS>(W.q[r] + n * (K / 8) + (int64_t)kb * 16, lg, b.w[r]);
-#pragma unroll
-      for (int h = 0; h < kG; ++h) {
-        const int64_t g = n * (K / GS) + (int64_t)kb * kG + h;
-        b.st[r][h] = W.s[r][g];
-        if (ZP) b.z[r][h] = W.z[r][g];
-      }
     }
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -278,12 +272,42 @@ __global__ __launch_bounds__(64 * kSkWaves) void w4a16_gated_skinny_kernel(
         b.a[t][kk] = *reinterpret_cast<const half8_t*>(ar[t] + (int64_t)kb * 128 +
                                                        8 * chunk_of<GS>(lg, kk));
   };
-  auto compute = [&](const Block& b) {
+  // group steps and zero points of four of the wave's blocks at a time, one per lane group (groups of
+  // 64: both of a block in one load), handed to all lane groups when their block comes
+  struct Steps {
+    uint32_t st[2], z[2];
+  };
+  Steps sv;
+  auto load_steps = [&](int kb) {
+    const int kl = kb + kSkWaves * lg < KB ? kb + kSkWaves * lg : KB - 1;
+    const int64_t g = n * (K / GS) + (int64_t)kl * kG;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (GS == 128) {
+        sv.st[r] = W.s[r][g];
+        if (ZP) sv.z[r] = W.z[r][g];
+      } else {
+        sv.st[r] = *reinterpret_cast<const uint32_t*>(W.s[r] + g);
+        if (ZP) sv.z[r] = *reinterpret_cast<const uint16_t*>(W.z[r] + g);
+      }
+    }
+  };
+  auto spread = [&](int j) {
+    Steps g;
+    const int from = 4 * (16 * (j & 3) + li);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      g.st[r] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)sv.st[r]);
+      if (ZP) g.z[r] = (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)sv.z[r]);
+    }
+    return g;
+  };
+  auto compute = [&](const Block& b, const Steps& g) {
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int h = 0; h < kG; ++h) {
-        const half2_t nsub = decode_nsub(ZP ? (float)b.z[r][h] : 8.0f);
+        const half2_t nsub = decode_nsub(ZP ? (float)((g.z[r] >> (8 * h)) & 0xFFu) : 8.0f);
         floatx4 part[MT];
 #pragma unroll
         for (int t = 0; t < MT; ++t) part[t] = floatx4{0.f, 0.f, 0.f, 0.f};
@@ -294,7 +318,7 @@ __global__ __launch_bounds__(64 * kSkWaves) void w4a16_gated_skinny_kernel(
           for (int t = 0; t < MT; ++t)
             part[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b.a[t][kk], wf, part[t], 0, 0, 0);
         }
-        const float st = h2f((uint16_t)b.st[r][h]);
+        const float st = h2f((uint16_t)(g.st[r] >> (16 * h)));
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -303,13 +327,20 @@ __global__ __launch_bounds__(64 * kSkWaves) void w4a16_gated_skinny_kernel(
   };
   // two blocks of the wave in flight
   Block b0, b1;
-  if (wave < KB) load(wave, b0);
-  for (int kb = wave; kb < KB; kb += 2 * kSkWaves) {
+  if (wave < KB) {
+    load_steps(wave);
+    load(wave, b0);
+  }
+  for (int kb = wave, j = 0; kb < KB; kb += 2 * kSkWaves, j += 2) {
     if (kb + kSkWaves < KB) load(kb + kSkWaves, b1);
-    compute(b0);
+    compute(b0, spread(j));
     if (kb + kSkWaves < KB) {
-      if (kb + 2 * kSkWaves < KB) load(kb + 2 * kSkWaves, b0);
-      compute(b1);
+      const Steps g = spread(j + 1);
+      if (kb + 2 * kSkWaves < KB) {
+        if ((j & 3) == 2) load_steps(kb + 2 * kSkWaves);
+        load(kb + 2 * kSkWaves, b0);
+      }
+      compute(b1, g);
     }
   }
 #pragma unroll
@@ -421,9 +452,10 @@ __global__ __launch_bounds__(256, 2) void w4a16_gated_tiled_kernel(
       }
     }
   };
-  // Group steps and zero points of four K steps at a time, K step b + lg in lane group lg (every lane
-  // loading the step that it uses was four times the loads, of two bytes a row each, and they bound
-  // the kernel); spread(j) hands those of the j-th K step to all lane groups.
+  // Group steps and zero points of four K steps at a time, K step b + lg in lane group lg; spread(j)
+  // hands those of the j-th to all lane groups. Every lane loading the step that it uses was four times
+  // the loads, each of two bytes in 16 rows, and they bound the kernel (17 rows of 28672 x 8192, groups
+  // of 64 with zero points: 167 us that way, 110 this way, 82 with none of them).
   struct Steps {
     uint32_t st[4], z[4];   // groups of 64: both groups' values
   };
@@ -721,9 +753,11 @@ __global__ __launch_bounds__(256) void w4a16_gated_finish_kernel(
 // Which kernel. The skinny one decodes 16 output channels' codes once for up to 32 rows but reads the
 // activations once per 16 channels; the tiled one with K slices is two launches. Skinny and
 // tiled, us (groups of 128):
-//   28672 x 8192: M = 16 105 and 103, M = 17 124 and 103, M = 32 160 and 106
-//   11008 x 4096: M = 16 24.4 and 28.3, M = 17 30.7 and 28.4, M = 32 37.7 and 30.0
-//   4096 x 4096:  M = 16 11.3 and 16.2, M = 32 13.5 and 18.2
+//   28672 x 8192: M = 8 72 and 75, M = 16 89 and 78
+//   11008 x 4096: M = 8 17.8 and 22.5, M = 16 21.5 and 23.2
+//   4096 x 4096:  M = 16 11.9 and 16.8, M = 32 12.5 and 16.8
+// (above 16 rows, before either loaded several steps' group steps at once: 17 x 28672 x 8192 124 and
+// 103, 17 x 11008 x 4096 30.7 and 28.4.)
 static bool skinny(int64_t M, int64_t N, int64_t K) {
   return M <= 16 || (M <= 32 && N * K <= (int64_t(1) << 24));
 }
@@ -733,14 +767,16 @@ GatedPlan w4a16_gated_plan(int64_t M, int64_t N, int64_t K, bool ckpt) {
   p.S = 1;
   if (!ckpt && skinny(M, N, K)) return p;
   p.tn = (N + kTN - 1) / kTN;
-  // 128 rows share a decoded weight tile (64 against 128 rows, us: 512 x 11008 x 4096 114 and 112,
-  // groups of 64 with zero points 210 and 148); with 16 such tiles or fewer the finer split of
-  // rows fills more CUs (256 x 1024 x 4096: 23 and 26, groups of 64 27 and 30)
-  p.bm = M > 64 && (M + 127) / 128 * p.tn > 16 ? 128 : M > 32 ? 64 : 32;
+  // 128 rows share a decoded weight tile (64 against 128 rows, us, groups of 128 and groups of 64 with
+  // zero points: 128 x 28672 x 8192 158 and 145, 224 and 185; 1024 x 11008 x 4096 198 and 179, 303
+  // and 229); with 64 such tiles or fewer the finer split of rows fills more CUs (256 x 4096 x 4096
+  // 33 and 40, 41 and 44; 256 x 1024 x 4096 23 and 27, 25 and 29). 32 rows where that is all: fewer
+  // registers, more workgroups per CU (17 x 11008 x 4096 23.6 and 26.2, 29.8 and 34.5 with 64).
+  p.bm = M > 64 && (M + 127) / 128 * p.tn > 64 ? 128 : M > 32 ? 64 : 32;
   p.tm = (M + p.bm - 1) / p.bm;
   p.Np = p.tn * kTN;
   const int64_t KB = K / 128, tiles = p.tm * p.tn;
-  if (tiles < 256) {   // two workgroups per CU, at least 4 steps each
+  if (tiles < 256) {   // two workgroups per CU (four of 32 rows), at least 4 steps each
     p.S = (p.bm == 32 ? 1024 : 512) / tiles;
     const int64_t smax = KB / 4;
     p.S = p.S > smax ? smax : p.S;

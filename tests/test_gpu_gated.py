@@ -57,7 +57,7 @@ def check(y, want, slack, dtype=torch.float16):
 FORWARD = [(1, 1, 128), (1, 130, 4224), (1, 64, 8320), (2, 257, 1024), (2, 40, 8192), (3, 16, 128),
            (16, 100, 1152), (17, 31, 2048), (32, 128, 640), (33, 1, 128), (64, 250, 4096),
            (65, 129, 1024), (128, 384, 256), (300, 200, 512), (300, 1100, 2048), (700, 4112, 128),
-           (17, 4200, 4096), (32, 4104, 4224)]
+           (17, 4200, 4096), (32, 4104, 4224), (300, 3000, 1024), (9, 200, 8192)]
 
 
 @pytest.mark.parametrize("group,zp,act", [(128, False, "silu"), (64, True, "gelu"),
@@ -75,7 +75,8 @@ def test_gated(awq, m, n, k, group, zp, act):
 
 @pytest.mark.parametrize("group,zp,act", [(128, False, "silu"), (64, True, "gelu")])
 @pytest.mark.parametrize("m,n,k", [(1, 16, 128), (3, 144, 4096), (64, 128, 256), (70, 272, 1024),
-                                   (300, 4112, 512), (300, 1104, 1024), (1000, 4096, 128)])
+                                   (300, 4112, 512), (300, 1104, 1024), (300, 3008, 1024),
+                                   (1000, 4096, 128)])
 def test_gated_ckpt(awq, m, n, k, group, zp, act):
     gate, up = (packed(n, k, group, zp, s + m) for s in (1, 2))
     a = np.random.default_rng(m + n + k).standard_normal((m, k)).astype(np.float16)
