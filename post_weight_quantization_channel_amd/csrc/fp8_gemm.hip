@@ -9,11 +9,12 @@
 // channel sits at which of the 32 bytes a lane supplies does not matter as long as both operands
 // agree; lane group lg (lane / 16) supplies the 16-byte chunks lg and lg + 4 of a block.
 //
-//   few rows  fp8_skinny_kernel (up to 8, or 48 on small weights): bound by the weight's bytes, which go from memory straight into
-//             the MFMA's registers; 8 waves of a workgroup share 16 weight rows and split K.
-//   else      fp8_tiled_kernel: tiles of 64, 128 or 256 rows, both operands through LDS, moved there by the buffer unit; with
-//             fewer tiles than CUs K is split over workgroups and the fp32 partials are added in
-//             slice order by fp8_sum_slices_kernel.
+//   few rows  fp8_skinny_kernel (up to 8, or 48 on small weights): bound by the weight's bytes,
+//             which go from memory straight into the MFMA's registers; 8 waves of a workgroup share
+//             16 weight rows and split K.
+//   else      fp8_tiled_kernel: tiles of 64, 128 or 256 rows, both operands through LDS, moved there
+//             by the buffer unit; with fewer tiles than CUs K is split over workgroups and the fp32
+//             partials are added in slice order by fp8_sum_slices_kernel.
 // Measured per call: 1 x 28672 x 8192 42 us (5.6 TB/s); 77 x 11000 x 4112 21 us (two launches);
 // 8192 x 11008 x 4096 400 us (1.85 PFLOP/s; matrix units busy 40% of the cycles at 2.0 GHz, the
 // scaling's vector instructions 31%).

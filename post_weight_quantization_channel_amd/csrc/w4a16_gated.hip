@@ -9,13 +9,14 @@
 // fp32 until H is rounded once, and until they are cut to 8 bits.
 //   M <= 2    w4a16_gated_gemv_kernel: bound by the codes' bytes; a wave owns one output channel,
 //             its gate row and its up row.
-//   few rows  w4a16_gated_skinny_kernel (up to 16, or 32 on small weights): MFMA, codes from memory to registers, K over 8 waves.
+//   few rows  w4a16_gated_skinny_kernel (up to 16, or 32 on small weights): MFMA, codes from memory
+//             to registers, K over 8 waves.
 //   else      w4a16_gated_tiled_kernel: 128 (64, 32) rows x 128 output channels; with few tiles K is
 //             split over workgroups and w4a16_gated_finish_kernel adds the slices in order and applies
 //             the activation. The 8-bit form always takes this path: 128 output channels of a
 //             tile are one block of the format.
 // Measured per call: 1 row of 11008 x 4096 11.6 us (46.5 MB, 4.0 TB/s); 16 rows 21.5 us; 512 rows,
-// groups of 64 with zero points, 148 us (0.62 PFLOP/s); 4096 rows with the 8-bit form 760 us (0.97
+// groups of 64 with zero points, 148 us (0.62 PFLOP/s); 4096 rows with the 8-bit form 746 us (0.99
 // PFLOP/s; matrix units busy 44% of the cycles at 1.96 GHz, the decode's and scaling's vector
 // instructions 42%).
 #include "fp8_format.h"
