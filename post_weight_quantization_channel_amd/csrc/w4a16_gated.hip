@@ -17,8 +17,8 @@
 //             tile are one block of the format.
 // Measured per call: 1 row of 11008 x 4096 11.6 us (46.5 MB, 4.0 TB/s); 16 rows 21.5 us; 512 rows,
 // groups of 64 with zero points, 148 us (0.62 PFLOP/s); 4096 rows with the 8-bit form 746 us (0.99
-// PFLOP/s; matrix units busy 44% of the cycles at 1.96 GHz, the decode's and scaling's vector
-// instructions 42%).
+// PFLOP/s; matrix units busy 46% of the cycles at 2.0 GHz, the decode's and scaling's vector
+// instructions 44%).
 #include "fp8_format.h"
 #include "gated_act.h"
 #include "kernels.h"
